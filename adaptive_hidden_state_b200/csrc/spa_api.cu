@@ -249,6 +249,7 @@ struct spa_model {
   void* chg_rows = nullptr;   // [B*N, d] compact changed rows (layer input of the next proxy)
   int32_t* chg0_idx = nullptr;  // [B*N] rows changed at layer 0 (the last unmasked positions)
   int chg0_u = 0;
+  std::vector<spa_q8_cache> q8;  // 8-bit K/V caches of the layers (empty: the layers' own)
 };
 
 static int check_desc(const spa_layer_desc* d) {
@@ -982,12 +983,176 @@ static int run_proxy(spa_layer* L, const void* H, const spa_layer_cache* c, floa
   return run_proxy_rows(L, H, nullptr, c->N, c, fill ? nullptr : L->ws->a_hat, score, fill, s);
 }
 
+// ---------------------------------------------------------------------------
+// 8-bit K/V cache
+// ---------------------------------------------------------------------------
+static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+static int check_device(const spa_workspace* ws) {
+  int dev = -1;
+  SPA_CK(cudaGetDevice(&dev));
+  if (dev != ws->device)
+    return fail(SPA_ERR_INVALID, "the workspace is on device %d, the current device is %d", ws->device, dev);
+  return SPA_OK;
+}
+
+static int check_q8(const spa_layer_desc& D, const spa_q8_cache* c) {
+  if (!c) return fail(SPA_ERR_INVALID, "null 8-bit cache");
+  if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale) return fail(SPA_ERR_INVALID, "null 8-bit cache buffer");
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes)) return fail(SPA_ERR_INVALID, "codes must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(c->k_scale) % 4 || reinterpret_cast<uintptr_t>(c->v_scale) % 4)
+    return fail(SPA_ERR_INVALID, "scales must be 4-byte aligned");
+  if (c->format != SPA_Q8_INT8 && c->format != SPA_Q8_E4M3)
+    return fail(SPA_ERR_INVALID, "format must be SPA_Q8_INT8 or SPA_Q8_E4M3");
+  if (c->B < 1 || c->N < 1 || c->n_kv_heads < 1) return fail(SPA_ERR_SHAPE, "non-positive cache dimension");
+  if (c->B > 65535 || c->n_kv_heads > 32767 || c->N > (1 << 30))
+    return fail(SPA_ERR_SHAPE, "B, n_kv_heads or N beyond the launch limits (65535, 32767, 2^30)");
+  if (c->head_dim != D.head_dim)
+    return fail(SPA_ERR_SHAPE, "cache head_dim %d differs from the workspace's %d", c->head_dim, D.head_dim);
+  if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128)
+    return fail(SPA_ERR_UNSUPPORTED, "an 8-bit cache takes head_dim 32, 64 or 128");
+  if (D.n_heads % c->n_kv_heads != 0)
+    return fail(SPA_ERR_SHAPE, "n_kv_heads %d does not divide the workspace's n_heads %d", c->n_kv_heads, D.n_heads);
+  if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128)
+    return fail(SPA_ERR_UNSUPPORTED, "block must be 16, 32, 64 or 128 tokens");
+  return SPA_OK;
+}
+
+// The 8-bit cache of a layer: the same sequences as its other caches, one kv head per query head.
+static int check_layer_q8(const spa_layer* L, const spa_layer_cache* c, const spa_q8_cache* q8) {
+  SPA_TRY(check_q8(L->desc, q8));
+  if (q8->B != c->B || q8->N != c->N || q8->n_kv_heads != L->desc.n_heads)
+    return fail(SPA_ERR_SHAPE, "the 8-bit cache's B, N or heads differ from the layer's");
+  return SPA_OK;
+}
+
+static int run_q8_write(spa_workspace* ws, const void* k_rows, const void* v_rows, int indexed, const int32_t* idx,
+                        int k, const spa_q8_cache* c, cudaStream_t s) {
+  const int bf = ws->desc.dtype == SPA_BF16;
+  Q8WriteParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.k_rows = k_rows; p.v_rows = v_rows; p.idx = idx; p.indexed = indexed;
+  p.k_codes = (uint8_t*)c->k_codes; p.v_codes = (uint8_t*)c->v_codes;
+  p.k_scale = c->k_scale; p.v_scale = c->v_scale;
+  p.B = c->B; p.N = c->N; p.k = k; p.n_kv = c->n_kv_heads; p.hd = c->head_dim; p.block = c->block;
+  p.err = ws->err;
+  const double rows = 2.0 * c->B * k * c->n_kv_heads * c->head_dim;
+  ProfScope ps(&ws->prof, SPA_PROF_MISC, rows * ((bf ? 2 : 4) + 1), 0.0, s);
+  const cudaError_t e = launch_q8_write(bf, c->format, p, s);
+  if (e != cudaSuccess) return fail(SPA_ERR_CUDA, "8-bit cache write launch: %s", cudaGetErrorString(e));
+  return SPA_OK;
+}
+
+static int run_q8_attention(spa_workspace* ws, const void* Q, const spa_q8_cache* c, const int32_t* lens, void* O,
+                            int k, cudaStream_t s) {
+  const spa_layer_desc& D = ws->desc;
+  const int bf = D.dtype == SPA_BF16;
+  Q8AttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.Q = Q; p.O = O; p.lens = lens;
+  p.k_codes = (const uint8_t*)c->k_codes; p.v_codes = (const uint8_t*)c->v_codes;
+  p.k_scale = c->k_scale; p.v_scale = c->v_scale;
+  p.sync = ws->attn_sync;
+  p.err = ws->err;
+  p.B = c->B; p.k = k; p.N = c->N; p.n_heads = D.n_heads; p.n_kv = c->n_kv_heads;
+  p.group = D.n_heads / c->n_kv_heads;
+  while ((1 << p.block_log2) < c->block) ++p.block_log2;
+  p.scale_log2 = 1.4426950408889634f / sqrtf((float)D.head_dim);
+  const double q = 2.0 * c->B * k * D.d * (bf ? 2 : 4), kv = 2.0 * c->B * c->N * c->n_kv_heads * c->head_dim;
+  ProfScope ps(&ws->prof, SPA_PROF_ATTN, q + kv, 4.0 * c->B * k * D.d * c->N, s);
+  const cudaError_t e = launch_q8_attention(bf, c->format, D.head_dim, p, ws->part_o, (size_t)ws->part_rows * D.d,
+                                            ws->attn_sync_len, ws->num_sms, s);
+  if (e != cudaSuccess) return fail(SPA_ERR_CUDA, "8-bit cache attention launch: %s", cudaGetErrorString(e));
+  return SPA_OK;
+}
+
+extern "C" int spa_q8_write(spa_workspace* ws, const spa_q8_cache* c, const void* k_rows, const void* v_rows,
+                            int indexed, const int32_t* idx, int k, void* stream) {
+  if (!ws) return fail(SPA_ERR_INVALID, "null workspace");
+  SPA_TRY(check_q8(ws->desc, c));
+  if (!k_rows || !v_rows) return fail(SPA_ERR_INVALID, "null rows");
+  if (!aligned16(k_rows) || !aligned16(v_rows)) return fail(SPA_ERR_INVALID, "rows must be 16-byte aligned");
+  if (indexed != 0 && indexed != 1) return fail(SPA_ERR_INVALID, "indexed must be 0 or 1");
+  if (k < 1 || k > c->N) return fail(SPA_ERR_SHAPE, "k=%d outside [1, N=%d]", k, c->N);
+  SPA_TRY(check_device(ws));
+  return run_q8_write(ws, k_rows, v_rows, indexed, idx, k, c, (cudaStream_t)stream);
+}
+
+extern "C" int spa_q8_read(spa_workspace* ws, const spa_q8_cache* c, const int32_t* idx, int k, void* k_out,
+                           void* v_out, void* stream) {
+  if (!ws) return fail(SPA_ERR_INVALID, "null workspace");
+  SPA_TRY(check_q8(ws->desc, c));
+  if (!k_out || !v_out) return fail(SPA_ERR_INVALID, "null output");
+  if (!aligned16(k_out) || !aligned16(v_out)) return fail(SPA_ERR_INVALID, "outputs must be 16-byte aligned");
+  if (k < 1 || (!idx && k > c->N)) return fail(SPA_ERR_SHAPE, "k=%d outside [1, N=%d]", k, c->N);
+  const long long chunks = (long long)c->n_kv_heads * c->head_dim / 16;
+  if ((long long)c->B * k > ((1LL << 31) - 1) * 256 / chunks) return fail(SPA_ERR_SHAPE, "more rows than a launch takes");
+  SPA_TRY(check_device(ws));
+  const int bf = ws->desc.dtype == SPA_BF16;
+  cudaStream_t s = (cudaStream_t)stream;
+  Q8ReadParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.k_codes = (const uint8_t*)c->k_codes; p.v_codes = (const uint8_t*)c->v_codes;
+  p.k_scale = c->k_scale; p.v_scale = c->v_scale;
+  p.idx = idx; p.k_out = k_out; p.v_out = v_out;
+  p.B = c->B; p.N = c->N; p.k = k; p.n_kv = c->n_kv_heads; p.hd = c->head_dim; p.block = c->block;
+  p.err = ws->err;
+  ProfScope ps(&ws->prof, SPA_PROF_MISC, 32.0 * c->B * k * chunks * ((bf ? 2 : 4) + 1), 0.0, s);
+  const cudaError_t e = launch_q8_read(bf, c->format, p, s);
+  if (e != cudaSuccess) return fail(SPA_ERR_CUDA, "8-bit cache read launch: %s", cudaGetErrorString(e));
+  return SPA_OK;
+}
+
+extern "C" int spa_q8_attention(spa_workspace* ws, const void* Q, const spa_q8_cache* c, const int32_t* lens,
+                                void* O, int k, void* stream) {
+  if (!ws) return fail(SPA_ERR_INVALID, "null workspace");
+  SPA_TRY(check_q8(ws->desc, c));
+  if (!Q || !O) return fail(SPA_ERR_INVALID, "null Q or O");
+  if (!aligned16(Q) || !aligned16(O)) return fail(SPA_ERR_INVALID, "Q and O must be 16-byte aligned");
+  if (k < 1 || k > (1 << 20)) return fail(SPA_ERR_SHAPE, "k=%d outside [1, 2^20]", k);
+  SPA_TRY(check_device(ws));
+  return run_q8_attention(ws, Q, c, lens, O, k, (cudaStream_t)stream);
+}
+
+// ---------------------------------------------------------------------------
+// token log probabilities
+// ---------------------------------------------------------------------------
+extern "C" int spa_token_logprobs(spa_workspace* ws, const void* logits, int dtype, long long rows, int vocab,
+                                  long long row_stride, const int32_t* tok, int top, float* logp, float* entropy,
+                                  int32_t* top_id, float* top_logp, void* stream) {
+  if (!ws) return fail(SPA_ERR_INVALID, "null workspace");
+  if (!logits || !tok || !logp || !entropy) return fail(SPA_ERR_INVALID, "null argument");
+  if (dtype != SPA_F32 && dtype != SPA_BF16) return fail(SPA_ERR_INVALID, "dtype must be SPA_F32 or SPA_BF16");
+  if (reinterpret_cast<uintptr_t>(logits) % (dtype == SPA_BF16 ? 2 : 4))
+    return fail(SPA_ERR_INVALID, "logits must be aligned to their element");
+  if (rows < 1 || rows > (1 << 27)) return fail(SPA_ERR_SHAPE, "rows outside [1, 2^27]");
+  if (vocab < 1 || vocab > (1 << 30)) return fail(SPA_ERR_SHAPE, "vocab outside [1, 2^30]");
+  if (row_stride < vocab) return fail(SPA_ERR_SHAPE, "row_stride below vocab");
+  if (top < 0 || top > 32) return fail(SPA_ERR_SHAPE, "top outside [0, 32]");
+  if (top > 0 && (!top_id || !top_logp)) return fail(SPA_ERR_INVALID, "null output for the alternatives");
+  SPA_TRY(check_device(ws));
+  cudaStream_t s = (cudaStream_t)stream;
+  LogpParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.logits = logits; p.ld = row_stride; p.V = vocab; p.top = top; p.tok = tok;
+  p.logp = logp; p.entropy = entropy; p.top_id = top_id; p.top_logp = top_logp;
+  p.err = ws->err;
+  ProfScope ps(&ws->prof, SPA_PROF_MISC, (double)rows * vocab * (dtype == SPA_BF16 ? 2 : 4) + rows * (12.0 + 8.0 * top),
+               5.0 * rows * vocab, s);
+  const cudaError_t e = launch_token_logprobs(dtype == SPA_BF16, p, (int)rows, ws->num_sms, s);
+  if (e != cudaSuccess) return fail(SPA_ERR_CUDA, "log-probability launch: %s", cudaGetErrorString(e));
+  return SPA_OK;
+}
+
 // Phases 2 and 3 for M = B * tps tokens; idx == null means every row (rho = 1).
 // Phase 2: x = RMSNorm(H[I]), Q/K/V with RoPE, K^c/V^c[I] <- K, V, and the
 // attention of the M = B * tps selected queries over the whole cache into
 // ws->O (compact rows); idx == null means every row (rho = 1).
+// q8: c's K^c and V^c only stage the fresh rows, which are then written into
+// the 8-bit cache the attention reads.
 static int run_attn_half(spa_layer* L, const void* H, const int32_t* idx, int tps,
-                         const spa_layer_cache* c, cudaStream_t s, bool x_ready) {
+                         const spa_layer_cache* c, cudaStream_t s, bool x_ready,
+                         const spa_q8_cache* q8 = nullptr) {
   spa_workspace* ws = L->ws;
   const spa_layer_desc& D = L->desc;
   const int d = D.d, M = c->B * tps, N = c->N;
@@ -1043,6 +1208,10 @@ static int run_attn_half(spa_layer* L, const void* H, const int32_t* idx, int tp
       SPA_TRY(run_simt(EPI_QKV, p, M, (3 * d + 127) / 128, s, prof,
                        Work{SPA_PROF_QKV, 3.0 * d * d * es + Md * es + 3.0 * Md * es, 6.0 * Md * d}));
     }
+  }
+  if (q8) {
+    SPA_TRY(run_q8_write(ws, c->k_cache, c->v_cache, 1, idx, tps, q8, s));
+    return run_q8_attention(ws, ws->Q, q8, nullptr, ws->O, tps, s);
   }
   // O = attention over the whole cache
   {
@@ -1276,8 +1445,9 @@ static int run_ffn_half(spa_layer* L, const void* H, const int32_t* idx, int tps
 // Phases 2 and 3 for M = B * tps tokens; idx == null means every row (rho = 1).
 static int run_block(spa_layer* L, const void* H, const int32_t* idx, int tps,
                      const spa_layer_cache* c, cudaStream_t s, bool x_ready = false,
-                     void* row_copy = nullptr, float* score_zero = nullptr) {
-  SPA_TRY(run_attn_half(L, H, idx, tps, c, s, x_ready));
+                     void* row_copy = nullptr, float* score_zero = nullptr,
+                     const spa_q8_cache* q8 = nullptr) {
+  SPA_TRY(run_attn_half(L, H, idx, tps, c, s, x_ready, q8));
   return run_ffn_half(L, H, idx, tps, c, s, L->ws->O, &L->ws->tmO, row_copy, score_zero);
 }
 
@@ -1328,7 +1498,8 @@ extern "C" int spa_partial_block(spa_layer* L, const void* H, const int32_t* idx
 // scores (P^c[I] = a_hat[I] now).
 static int layer_step_impl(spa_layer* L, const void* H, const spa_layer_cache* c, int k, int32_t* idx,
                            cudaStream_t s, float* a_hat, float* score, const void* chg,
-                           const int32_t* chg_idx, int chg_tps, void* row_copy) {
+                           const int32_t* chg_idx, int chg_tps, void* row_copy,
+                           const spa_q8_cache* q8 = nullptr) {
   const spa_layer_desc& D = L->desc;
   spa_workspace* ws = L->ws;
   if (!idx) return fail(SPA_ERR_INVALID, "null idx");
@@ -1355,7 +1526,7 @@ static int layer_step_impl(spa_layer* L, const void* H, const spa_layer_cache* c
     e = launch_topk_select(score, c->B, c->N, k, idx, a_hat, c->p_cache, D.r, ws->err, s);
   }
   if (e != cudaSuccess) return fail(SPA_ERR_CUDA, "select launch: %s", cudaGetErrorString(e));
-  return run_block(L, H, idx, k, c, s, x_ready, row_copy, state ? score : nullptr);
+  return run_block(L, H, idx, k, c, s, x_ready, row_copy, state ? score : nullptr, q8);
 }
 
 extern "C" int spa_layer_step(spa_layer* L, const void* H, const spa_layer_cache* c, int k,
@@ -1365,6 +1536,16 @@ extern "C" int spa_layer_step(spa_layer* L, const void* H, const spa_layer_cache
   SPA_TRY(check_cache(L, c));
   return layer_step_impl(L, H, c, k, idx, (cudaStream_t)stream, nullptr, nullptr, nullptr, nullptr, 0,
                          nullptr);
+}
+
+extern "C" int spa_layer_step_q8(spa_layer* L, const void* H, const spa_layer_cache* c, const spa_q8_cache* q8,
+                                 int k, int32_t* idx, void* stream) {
+  if (!L) return fail(SPA_ERR_INVALID, "null layer");
+  SPA_TRY(check_H(H));
+  SPA_TRY(check_cache(L, c));
+  SPA_TRY(check_layer_q8(L, c, q8));
+  return layer_step_impl(L, H, c, k, idx, (cudaStream_t)stream, nullptr, nullptr, nullptr, nullptr, 0,
+                         nullptr, q8);
 }
 
 // Unit rows of the attention outputs ws->O (M rows of r = d elements) into
@@ -1381,22 +1562,35 @@ static int score_attn_rows(spa_layer* L, const spa_layer_cache* c, int fill, cud
   return SPA_OK;
 }
 
+static int full_block_impl(spa_layer* L, const void* H, const spa_layer_cache* c, int fill_proxy,
+                           cudaStream_t s, const spa_q8_cache* q8) {
+  if (fill_proxy < 0 || fill_proxy > 2) return fail(SPA_ERR_INVALID, "fill_proxy must be 0, 1 or 2");
+  if (fill_proxy == 2) {
+    // the attention-output identifier's fill: P^c = unit attention output of every row
+    if (L->desc.r != L->desc.d) return fail(SPA_ERR_SHAPE, "the attention-output identifier needs r = d");
+    SPA_TRY(run_attn_half(L, H, nullptr, c->N, c, s, false, q8));
+    SPA_TRY(score_attn_rows(L, c, 1, s));
+    return run_ffn_half(L, H, nullptr, c->N, c, s, L->ws->O, &L->ws->tmO, nullptr, nullptr);
+  }
+  if (fill_proxy) SPA_TRY(run_proxy(L, H, c, nullptr, 1, s));
+  return run_block(L, H, nullptr, c->N, c, s, false, nullptr, nullptr, q8);
+}
+
 extern "C" int spa_full_block(spa_layer* L, const void* H, const spa_layer_cache* c, int fill_proxy,
                               void* stream) {
   if (!L) return fail(SPA_ERR_INVALID, "null layer");
   SPA_TRY(check_H(H));
   SPA_TRY(check_cache(L, c));
-  if (fill_proxy < 0 || fill_proxy > 2) return fail(SPA_ERR_INVALID, "fill_proxy must be 0, 1 or 2");
-  cudaStream_t s = (cudaStream_t)stream;
-  if (fill_proxy == 2) {
-    // the attention-output identifier's fill: P^c = unit attention output of every row
-    if (L->desc.r != L->desc.d) return fail(SPA_ERR_SHAPE, "the attention-output identifier needs r = d");
-    SPA_TRY(run_attn_half(L, H, nullptr, c->N, c, s, false));
-    SPA_TRY(score_attn_rows(L, c, 1, s));
-    return run_ffn_half(L, H, nullptr, c->N, c, s, L->ws->O, &L->ws->tmO, nullptr, nullptr);
-  }
-  if (fill_proxy) SPA_TRY(run_proxy(L, H, c, nullptr, 1, s));
-  return run_block(L, H, nullptr, c->N, c, s);
+  return full_block_impl(L, H, c, fill_proxy, (cudaStream_t)stream, nullptr);
+}
+
+extern "C" int spa_full_block_q8(spa_layer* L, const void* H, const spa_layer_cache* c, const spa_q8_cache* q8,
+                                 int fill_proxy, void* stream) {
+  if (!L) return fail(SPA_ERR_INVALID, "null layer");
+  SPA_TRY(check_H(H));
+  SPA_TRY(check_cache(L, c));
+  SPA_TRY(check_layer_q8(L, c, q8));
+  return full_block_impl(L, H, c, fill_proxy, (cudaStream_t)stream, q8);
 }
 
 extern "C" int spa_layer_step_attn_identifier(spa_layer* L, const void* H, const spa_layer_cache* c, int k,
@@ -1537,6 +1731,25 @@ extern "C" int spa_model_set_incremental_proxy(spa_model* m, int enable) {
   return SPA_OK;
 }
 
+extern "C" int spa_model_set_q8(spa_model* m, const spa_q8_cache* caches) {
+  if (!m) return fail(SPA_ERR_INVALID, "null model");
+  try {
+    std::vector<spa_q8_cache> v;
+    if (caches) {
+      v.assign(caches, caches + m->desc.n_layers);
+      for (int l = 0; l < m->desc.n_layers; ++l) SPA_TRY(check_layer_q8(m->layers[l], &m->caches[l], &v[l]));
+    }
+    m->q8.swap(v);
+  } catch (const std::bad_alloc&) {
+    return fail(SPA_ERR_NOMEM, "host allocation failed");
+  }
+  // a captured step reads the caches it was captured with
+  if (m->graph) cudaGraphExecDestroy(m->graph);
+  m->graph = nullptr;
+  m->inc_valid = false;
+  return SPA_OK;
+}
+
 extern "C" int spa_model_embed(spa_model* m, const int32_t* tokens, void* stream) {
   if (!m || !tokens) return fail(SPA_ERR_INVALID, "null argument");
   m->inc_valid = false;  // every row of the layer-0 input may change
@@ -1555,22 +1768,25 @@ static int decode_layers_impl(spa_model* m, int full, cudaStream_t s) {
   const spa_layer_desc& D = ws->desc;
   const int L = m->desc.n_layers, B = m->desc.B, N = m->desc.N;
   const size_t rows = (size_t)B * N;
-  void* stream = (void*)s;
   const bool inc = m->inc;
   const bool use_chg = inc && m->inc_valid && !full;
   const int r = D.r;
+  const bool has_q8 = !m->q8.empty();
   for (int l = 0; l < L; ++l) {
     const void* H = (l == 0) ? m->h0 : m->caches[l - 1].h_cache;
     spa_layer* ly = m->layers[l];
     const spa_layer_cache* c = &m->caches[l];
+    const spa_q8_cache* q8 = has_q8 ? &m->q8[l] : nullptr;
     float* A = inc ? m->ahat_all + (size_t)l * rows * r : nullptr;
     float* S = inc ? m->score_all + (size_t)l * rows : nullptr;
     if (full == 1 && inc) {
       // the rho = 1 fill also sets the proxy state: a_hat = P^c, score 0
       SPA_TRY(run_proxy_rows(ly, H, nullptr, N, c, A, S, 1, s));
-      SPA_TRY(run_block(ly, H, nullptr, N, c, s));
+      SPA_TRY(run_block(ly, H, nullptr, N, c, s, false, nullptr, nullptr, q8));
     } else if (full) {
-      SPA_TRY(spa_full_block(ly, H, c, full == 1 ? 1 : 0, stream));
+      SPA_TRY(check_H(H));
+      SPA_TRY(check_cache(ly, c));
+      SPA_TRY(full_block_impl(ly, H, c, full == 1 ? 1 : 0, s, q8));
     } else if (inc) {
       const int32_t* ci = l == 0 ? m->chg0_idx : m->idx_all + (size_t)(l - 1) * rows;
       const int ctps = l == 0 ? m->chg0_u : m->k[l - 1];
@@ -1578,9 +1794,12 @@ static int decode_layers_impl(spa_model* m, int full, cudaStream_t s) {
       SPA_TRY(check_cache(ly, c));
       SPA_TRY(layer_step_impl(ly, H, c, m->k[l], m->idx_all + (size_t)l * rows, s, A, S,
                               use_chg ? m->chg_rows : nullptr, use_chg ? ci : nullptr, use_chg ? ctps : 0,
-                              m->chg_rows));
+                              m->chg_rows, q8));
     } else {
-      SPA_TRY(spa_layer_step(ly, H, c, m->k[l], m->idx_all + (size_t)l * rows, stream));
+      SPA_TRY(check_H(H));
+      SPA_TRY(check_cache(ly, c));
+      SPA_TRY(layer_step_impl(ly, H, c, m->k[l], m->idx_all + (size_t)l * rows, s, nullptr, nullptr, nullptr,
+                              nullptr, 0, nullptr, q8));
     }
   }
   // the proxy state follows the caches after a fill or a cached step in
@@ -1592,9 +1811,10 @@ static int decode_layers_impl(spa_model* m, int full, cudaStream_t s) {
 
 // Final RMSNorm at the u positions pos ([B, u]) of the last layer's output,
 // LM head, and per row the argmax id (lowest on ties) into tok_out; with
-// conf_out, also that id's softmax probability.
+// conf_out, also that id's softmax probability.  With logits ([B * u, vocab]
+// fp32) the LM head's fp32 sums go there instead.
 static int lm_head_impl(spa_model* m, const int32_t* pos, int u, int32_t* tok_out, float* conf_out,
-                        cudaStream_t s) {
+                        cudaStream_t s, float* logits = nullptr) {
   spa_workspace* ws = m->layers[0]->ws;
   const spa_layer_desc& D = ws->desc;
   const int L = m->desc.n_layers, B = m->desc.B, N = m->desc.N, d = D.d;
@@ -1620,13 +1840,15 @@ static int lm_head_impl(spa_model* m, const int32_t* pos, int u, int32_t* tok_ou
   ep.amax_val = m->amax_val;
   ep.amax_idx = m->amax_idx;
   ep.amax_sum = conf_out ? m->amax_sum : nullptr;
+  ep.out = logits;
   ep.err = ws->err;
+  const int mode = logits ? EPI_PROXY_RAW : EPI_ARGMAX;
   int tiles = m->lm_tiles;
   if (D.dtype == SPA_BF16 && M <= 256) {
     TcWsParams p;
     std::memset(&p, 0, sizeof(p));
     p.tmW[0] = m->tm_lm; p.b_mode = B_SINGLE; p.b_rows_per_src = m->desc.vocab; p.ep = ep;
-    SPA_TRY(run_ws(EPI_ARGMAX, false, p, ws, ws->X, M, d, m->desc.vocab, s, &ws->prof, wl));
+    SPA_TRY(run_ws(mode, false, p, ws, ws->X, M, d, m->desc.vocab, s, &ws->prof, wl));
     tiles = p.ep.n_tiles;
   } else if (D.dtype == SPA_BF16) {
     tiles = (m->desc.vocab + 255) / 256;
@@ -1636,15 +1858,16 @@ static int lm_head_impl(spa_model* m, const int32_t* pos, int u, int32_t* tok_ou
     p.tmA = ws->tmX;
     p.tmB[0] = m->tm_lm;
     p.K = d; p.b_mode = B_SINGLE; p.b_rows_per_src = m->desc.vocab; p.ep = ep;
-    SPA_TRY(run_tc(EPI_ARGMAX, 256, p, M, tiles, 1, s, &ws->prof, wl));
+    SPA_TRY(run_tc(mode, 256, p, M, tiles, 1, s, &ws->prof, wl));
   } else {
     ep.n_tiles = tiles;
     SimtGemmParams p;
     std::memset(&p, 0, sizeof(p));
     p.A = (const float*)ws->X; p.B[0] = (const float*)m->lm_head;
     p.K = d; p.b_mode = B_SINGLE; p.b_rows_per_src = m->desc.vocab; p.ep = ep;
-    SPA_TRY(run_simt(EPI_ARGMAX, p, M, m->lm_tiles, s, &ws->prof, wl));
+    SPA_TRY(run_simt(mode, p, M, m->lm_tiles, s, &ws->prof, wl));
   }
+  if (logits) return SPA_OK;
   {
     ProfScope ps(&ws->prof, SPA_PROF_MISC, 8.0 * M * m->lm_tiles, 0.0, s);
     e = conf_out ? launch_confidence_reduce(m->amax_val, m->amax_idx, m->amax_sum, M, tiles, tok_out, conf_out, s)
@@ -1695,6 +1918,13 @@ extern "C" int spa_decode_confidence(spa_model* m, const int32_t* pos, int u, in
   if (!m || !pos || !tok_out || !conf_out) return fail(SPA_ERR_INVALID, "null argument");
   if (u < 1 || u > m->desc.N) return fail(SPA_ERR_SHAPE, "u=%d outside [1, N]", u);
   return lm_head_impl(m, pos, u, tok_out, conf_out, (cudaStream_t)stream);
+}
+
+extern "C" int spa_decode_logits(spa_model* m, const int32_t* pos, int u, float* logits, void* stream) {
+  if (!m || !pos || !logits) return fail(SPA_ERR_INVALID, "null argument");
+  if (u < 1 || u > m->desc.N) return fail(SPA_ERR_SHAPE, "u=%d outside [1, N]", u);
+  if (!aligned16(logits)) return fail(SPA_ERR_INVALID, "logits must be 16-byte aligned");
+  return lm_head_impl(m, pos, u, nullptr, nullptr, (cudaStream_t)stream, logits);
 }
 
 extern "C" int spa_model_write_tokens(spa_model* m, const int32_t* pos, const int32_t* tok, int u,

@@ -304,9 +304,15 @@ __device__ void run_epilogue(const float* tile, int ld, int row_begin, int row_e
     for (int it = tid; it < nrows * C4; it += nthr) {
       const int row = row_begin + it / C4, c = (it % C4) * 4;
       const int t = gm0 + row, gn = gn0 + c;
-      if (t >= ep.M || gn >= ep.n_out) continue;  // n_out is a multiple of 4
-      *reinterpret_cast<float4*>(out + (size_t)t * ep.n_out + gn) =
-          *reinterpret_cast<const float4*>(tile + row * ld + c);
+      if (t >= ep.M || gn >= ep.n_out) continue;
+      const float4 v = *reinterpret_cast<const float4*>(tile + row * ld + c);
+      float* dst = out + (size_t)t * ep.n_out + gn;
+      if (ep.n_out % 4 == 0) {
+        *reinterpret_cast<float4*>(dst) = v;
+      } else {  // the logits of a vocabulary that is no multiple of 4
+        const float e[4] = {v.x, v.y, v.z, v.w};
+        for (int q = 0; q < 4 && gn + q < ep.n_out; ++q) dst[q] = e[q];
+      }
     }
   } else if constexpr (MODE == EPI_ARGMAX) {
     const int lane = tid & 31, wid = tid >> 5, nw = nthr >> 5;
@@ -1171,7 +1177,8 @@ static int ws_max_clusters(int splits) {
   X(EPI_RESID, 1) X(EPI_RESID, 2) X(EPI_RESID, 4)                         \
   X(EPI_SWIGLU, 2) X(EPI_SWIGLU, 4)                                       \
   X(EPI_RESID_SCATTER, 1) X(EPI_RESID_SCATTER, 2) X(EPI_RESID_SCATTER, 4) \
-  X(EPI_ARGMAX, 1) X(EPI_ARGMAX, 2) X(EPI_ARGMAX, 4)
+  X(EPI_ARGMAX, 1) X(EPI_ARGMAX, 2) X(EPI_ARGMAX, 4)                      \
+  X(EPI_PROXY_RAW, 1) X(EPI_PROXY_RAW, 2) X(EPI_PROXY_RAW, 4)
 
 cudaError_t launch_tc_ws(int mode, int nacc, const TcWsParams& p, int n_tiles, int splits,
                          cudaStream_t stream) {
@@ -1335,6 +1342,7 @@ cudaError_t launch_simt_gemm(int mode, const SimtGemmParams& p, int m_tiles, int
     case EPI_RESID_SCATTER: return launch_k(simt_gemm_kernel<EPI_RESID_SCATTER>, grid, block, 0, stream, p);
     case EPI_PROXY: return launch_k(simt_gemm_kernel<EPI_PROXY>, grid, block, 0, stream, p);
     case EPI_ARGMAX: return launch_k(simt_gemm_kernel<EPI_ARGMAX>, grid, block, 0, stream, p);
+    case EPI_PROXY_RAW: return launch_k(simt_gemm_kernel<EPI_PROXY_RAW>, grid, block, 0, stream, p);
     default: return cudaErrorInvalidValue;
   }
 }

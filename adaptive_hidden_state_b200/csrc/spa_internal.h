@@ -12,6 +12,7 @@ enum : int {
   DEVERR_TIMEOUT = 1,  // a bounded wait ran out
   DEVERR_INDEX = 2,    // a gather/scatter index fell outside [0, N)
   DEVERR_SHAPE = 4,    // a launch saw a shape it cannot handle
+  DEVERR_VALUE = 8,    // a NaN or an infinity where the 8-bit cache cannot hold one
 };
 
 // What a GEMM does with its fp32 accumulator tile (rows = tokens, columns =
@@ -24,7 +25,7 @@ enum EpiMode : int {
   EPI_RESID_SCATTER = 4,  // H^c[b, I[t]] = acc + H1[t]
   EPI_PROXY = 5,          // a_hat = acc/|acc|; s = 1/2|a_hat - P^c|^2 (or fill P^c)
   EPI_ARGMAX = 6,         // per-tile (max, argmax) of the logits of each row
-  EPI_PROXY_RAW = 7,      // out[t, n] = acc (fp32): the proxy of a wide r, finished per row
+  EPI_PROXY_RAW = 7,      // out[t, n] = acc (fp32): the proxy of a wide r, finished per row; logits
 };
 
 // How column tile n maps to rows of the weight sources.
@@ -271,6 +272,55 @@ cudaError_t launch_confidence_reduce(const float* val, const int32_t* idx, const
 // arrives on; else until *flag == expect), for tests of the time-out path.
 cudaError_t launch_wait_probe(const int* flag, int expect, unsigned long long limit_ns, int* err,
                               cudaStream_t stream);
+// ---- 8-bit K/V cache (spa_q8.cu, spa_q8_attn.cu) ----
+// codes [B, N, n_kv * hd], scales [B, ceil(N / block), n_kv].
+struct Q8WriteParams {
+  const void *k_rows, *v_rows;  // [B, k, n_kv * hd], or with indexed [B, N, n_kv * hd]
+  const int32_t* idx;           // [B, k] cache rows (null: 0 .. k - 1)
+  uint8_t *k_codes, *v_codes;
+  float *k_scale, *v_scale;
+  int B, N, k, n_kv, hd, block, indexed;
+  int* err;
+};
+struct Q8ReadParams {
+  const uint8_t *k_codes, *v_codes;
+  const float *k_scale, *v_scale;
+  const int32_t* idx;           // [B, k] cache rows (null: 0 .. k - 1)
+  void *k_out, *v_out;          // [B, k, n_kv * hd]
+  int B, N, k, n_kv, hd, block;
+  int* err;
+};
+struct Q8AttnParams {
+  const void* Q;                // [B, k, n_heads * hd]
+  void* O;
+  const uint8_t *k_codes, *v_codes;
+  const float *k_scale, *v_scale;
+  const int32_t* lens;          // [B] rows of each sequence that count (null: N)
+  float *part_o, *part_ml;      // key shares: unnormalised rows, (m, l) pairs
+  int* sync;                    // arrivals per row tile, zero between launches
+  int* err;
+  int B, k, N, n_heads, n_kv, group, block_log2, tiles, splits;
+  float scale_log2;             // log2(e) / sqrt(hd)
+};
+// dtype 0 fp32, 1 bf16; fmt 0 int8, 1 e4m3; hd 32, 64 or 128; block 16, 32, 64 or 128.
+cudaError_t launch_q8_write(int dtype, int fmt, const Q8WriteParams& p, cudaStream_t stream);
+cudaError_t launch_q8_read(int dtype, int fmt, const Q8ReadParams& p, cudaStream_t stream);
+// part: scratch for the key shares, sync: [sync_len] ints, zero between launches.
+cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, float* part, size_t part_floats,
+                                size_t sync_len, int num_sms, cudaStream_t stream);
+// Per row of logits [rows, V] (row stride ld elements): log probability of
+// tok, entropy, and the `top` largest (ties to the lowest id).
+struct LogpParams {
+  const void* logits;
+  long long ld;
+  int V, top;
+  const int32_t* tok;
+  float *logp, *entropy;
+  int32_t* top_id;
+  float* top_logp;
+  int* err;
+};
+cudaError_t launch_token_logprobs(int dtype, const LogpParams& p, int rows, int num_sms, cudaStream_t stream);
 // Copies a [rows] int32 array (device) element-wise.
 cudaError_t launch_copy_i32(const int32_t* src, int32_t* dst, int n, cudaStream_t stream);
 

@@ -1,0 +1,79 @@
+// Codes of the 8-bit K/V cache on the device: their formats, the power-of-two
+// scale of a block, and the exact conversion of codes to bf16 pairs.
+//
+// A code's value is its format's value times the scale of its (block of
+// tokens, head).  The scale is a power of two, so v / s is exact in fp32: the
+// code of a value depends on the value and the scale alone, and a row that
+// stays in a block is re-scaled without loss when the block's scale falls and
+// rounded once when it grows.  (With s = max / qmax every change of scale
+// would round every remaining row, and the cache rewrites scattered rows in
+// every step.)  The price is up to one bit of an int8 code's range.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "spa_device.cuh"
+
+namespace spa {
+
+constexpr int kQ8Int8 = 0, kQ8E4m3 = 1;
+
+template <int FMT> __device__ __forceinline__ float q8_max() { return FMT == kQ8Int8 ? 127.f : 448.f; }
+
+// Smallest power of two s >= 2^-126 with a <= qmax * s (0 for a = 0; a finite).
+// 127 = 1.984375 * 2^6 and 448 = 1.75 * 2^8: compare mantissas, adjust exponents.
+template <int FMT> __device__ __forceinline__ float q8_scale(float a) {
+  if (!(a > 0.f)) return 0.f;
+  const uint32_t u = __float_as_uint(a);
+  const int e = (int)(u >> 23);  // biased; 0 for a subnormal, which ends at the lower bound below
+  const uint32_t m = u & 0x7FFFFFu;
+  constexpr uint32_t mq = FMT == kQ8Int8 ? 0x7E0000u : 0x600000u;
+  constexpr int eq = FMT == kQ8Int8 ? 6 : 8;
+  int t = e - eq + (m > mq ? 1 : 0);
+  if (t < 1) t = 1;  // 2^-126
+  return __uint_as_float((uint32_t)t << 23);
+}
+// 1 / s of a scale q8_scale returned (2^-126 .. 2^122): exact.
+__device__ __forceinline__ float q8_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
+
+// Two codes of the pair of values (a, b), already divided by the scale.
+template <int FMT> __device__ __forceinline__ uint32_t q8_encode2(float a, float b) {
+  if constexpr (FMT == kQ8Int8) {
+    return ((uint32_t)__float2int_rn(a) & 0xFFu) | (((uint32_t)__float2int_rn(b) & 0xFFu) << 8);
+  } else {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  }
+}
+
+// Pair of bf16 from the two codes at byte positions 0 and 2 of t (the other
+// bytes are ignored): exact, since a code has at most 8 significant bits.
+//   int8:  0x4300 | (c & 0x7F) is 128 + (c & 0x7F) and 0x4300 | (c & 0x80) is
+//          128 or 256; their difference is the signed value.
+//   e4m3:  the 7 low bits at bf16's exponent and mantissa positions read as
+//          the value times 2^-120 (subnormals included).
+template <int FMT> __device__ __forceinline__ uint32_t q8_to_bf162_lo(uint32_t t) {
+  __nv_bfloat162 r;
+  if constexpr (FMT == kQ8Int8) {
+    const uint32_t lo = (t & 0x007F007Fu) | 0x43004300u, hi = (t & 0x00800080u) | 0x43004300u;
+    r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&hi));
+  } else {
+    const uint32_t w = ((t & 0x007F007Fu) << 4) | ((t & 0x00800080u) << 8);
+    const uint32_t f = 0x7B807B80u;  // 2^120
+    r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&f));
+  }
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+// Four codes of a word -> two bf16 pairs (bytes 0, 1 and bytes 2, 3).
+template <int FMT> __device__ __forceinline__ void q8_word_to_bf16(uint32_t w, uint32_t& p01, uint32_t& p23) {
+  p01 = q8_to_bf162_lo<FMT>(__byte_perm(w, 0, 0x4140));
+  p23 = q8_to_bf162_lo<FMT>(__byte_perm(w, 0, 0x4342));
+}
+
+// One code as float.
+template <int FMT> __device__ __forceinline__ float q8_value(uint32_t byte) {
+  if constexpr (FMT == kQ8Int8) return (float)(int8_t)(uint8_t)byte;
+  __nv_fp8_e4m3 v;
+  v.__x = (__nv_fp8_storage_t)byte;
+  return (float)v;
+}
+
+}  // namespace spa

@@ -1,0 +1,423 @@
+// Attention over the 8-bit K/V cache: O = softmax(Q K^T / sqrt(hd)) V with
+// K = codes * scale, V = codes * scale, over the first len_b rows of each
+// sequence.  The `group` query heads that share a kv head and the k queries
+// of a sequence form the R = k * group query rows of that kv head (row
+// r = query r / group, head r % group).
+//
+// The codes are exact in bf16 (at most 8 significant bits), so the products
+// run on the tensor cores in bf16 with fp32 sums, and the scales stay outside
+// them: a key block's scale multiplies its scores, a value block's scale the
+// probabilities before they are rounded to bf16 (a power of two there moves
+// no rounding).
+//
+// q8_attn_rows_kernel (below) takes 16 query rows per CTA.
+#include <cstring>
+
+#include "spa_q8.cuh"
+
+namespace spa {
+
+// ---------------------------------------------------------------------------
+// Row kernel: 16 query rows of one kv head and one contiguous share of its
+// keys per CTA.
+//
+// Each of the four warps walks its own chunks of 16 keys with its own running
+// maximum m, sum l and output, fed by its own ring of asynchronous 16-byte
+// copies (no barrier between warps), so the copies of three chunks are in
+// flight per warp.  m16n8k16 products: the order of the head elements within
+// a step is free as long as Q and K agree, so a thread reads its HD/4
+// elements of a key as whole 16-byte pieces; likewise the columns of V, of
+// which a thread takes HD/8 consecutive ones.  The ring's 16-byte pieces are
+// permuted within 128-byte lines so that these reads hit every bank once.
+//
+// fp32 queries: Q and P are each the sum of three bf16 terms (24 bits), so
+// three products give the fp32 result to fp32 accuracy.
+//
+// The warps' results are joined in shared memory in warp order, and the key
+// shares of a row tile through global scratch by the last CTA to arrive, in
+// share order: the result does not depend on timing.
+// ---------------------------------------------------------------------------
+constexpr int kRWarps = 4, kRThreads = kRWarps * 32;
+constexpr int kRKeys = 16;    // keys of a chunk
+constexpr int kRStages = 4;   // chunks in a warp's ring
+
+template <int HD> struct RowCfg {
+  static constexpr int kStageBytes = 2 * kRKeys * HD + 16;  // K codes, V codes, the two scales
+  static constexpr int kRing = kRWarps * kRStages * kStageBytes;
+  static constexpr int kJoin = kRWarps * 16 * (HD + 2) * 4;
+  static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Byte offset of 16-byte piece c of row r (16 rows of HD bytes).
+template <int HD> __device__ __forceinline__ int row_piece(int r, int c) {
+  constexpr int RPL = 128 / HD, CPR = HD / 16, MUL = HD == 128 ? 1 : 2;
+  const int line = r / RPL;
+  return line * 128 + ((((r % RPL) * CPR + c) ^ ((MUL * line) & 7)) << 4);
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// The leading bf16 term of (a, b), which is subtracted from them.
+__device__ __forceinline__ uint32_t split_bf16(float& a, float& b) {
+  const uint32_t w = pack_bf16(a, b);
+  a -= __uint_as_float(w << 16);
+  b -= __uint_as_float(w & 0xFFFF0000u);
+  return w;
+}
+
+// NB bytes of shared memory at p into words.
+template <int NB> __device__ __forceinline__ void lds_words(uint32_t (&w)[NB / 4], const uint8_t* p) {
+  if constexpr (NB == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if constexpr (NB == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+template <typename T, int HD, int FMT>
+__global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int NT = sizeof(T) == 4 ? 3 : 1;  // bf16 terms of a query element and of a probability
+  constexpr int KW = HD / 16;                 // words of a key a thread reads = k16 steps of Q K^T
+  constexpr int VB = HD / 8;                  // consecutive columns of V a thread reads = n8 tiles of P V
+  constexpr int SB = RowCfg<HD>::kStageBytes;
+  __shared__ int s_last;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+  const int S = p.splits, tile = blockIdx.x / S, sp = blockIdx.x % S, h = blockIdx.y, b = blockIdx.z;
+  const int R = p.k * p.group;
+  int len = p.N;
+  if (p.lens) {
+    len = __ldg(p.lens + b);
+    if (len < 0 || len > p.N) {
+      if (threadIdx.x == 0) report_error(p.err, DEVERR_INDEX, 711);
+      len = min(max(len, 0), p.N);
+    }
+  }
+  const int nch = (len + kRKeys - 1) / kRKeys;
+  const int c0 = (int)((long long)sp * nch / S), c1 = (int)((long long)(sp + 1) * nch / S);
+
+  // this thread's Q elements: rows g and g + 8, elements tig * HD/4 ..
+  uint32_t q[NT][KW][4];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = tile * 16 + g + 8 * half;
+    const bool ok = r < R;
+    const int i = ok ? r / p.group : 0, gh = ok ? r % p.group : 0;
+    const T* src = reinterpret_cast<const T*>(p.Q) +
+                   (((size_t)b * p.k + i) * p.n_heads + (size_t)h * p.group + gh) * HD + tig * (HD / 4);
+#pragma unroll
+    for (int s = 0; s < KW; ++s) {
+      if constexpr (NT == 1) {
+        const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(src) + s) : make_uint2(0u, 0u);
+        q[0][s][half] = w.x;
+        q[0][s][2 + half] = w.y;
+      } else {
+        float4 v = ok ? __ldg(reinterpret_cast<const float4*>(src) + s) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          q[n][s][half] = split_bf16(v.x, v.y);
+          q[n][s][2 + half] = split_bf16(v.z, v.w);
+        }
+      }
+    }
+  }
+
+  const size_t width = (size_t)p.n_kv * HD;
+  const uint8_t* kbase = p.k_codes + (size_t)b * p.N * width + (size_t)h * HD;
+  const uint8_t* vbase = p.v_codes + (size_t)b * p.N * width + (size_t)h * HD;
+  const int nb = (p.N + (1 << p.block_log2) - 1) >> p.block_log2;
+  const float* ksc = p.k_scale + (size_t)b * nb * p.n_kv + h;
+  const float* vsc = p.v_scale + (size_t)b * nb * p.n_kv + h;
+  uint8_t* ring = smem + warp * kRStages * SB;
+
+  auto fetch = [&](int c, int st) {  // chunk c (always committed, empty past the end)
+    if (c < c1) {
+      uint8_t* dst = ring + st * SB;
+#pragma unroll
+      for (int it = 0; it < 2 * kRKeys * (HD / 16) / 32; ++it) {
+        const int e = it * 32 + lane;
+        const int is_v = e / (kRKeys * (HD / 16)), f = e % (kRKeys * (HD / 16));
+        const int r = f / (HD / 16), cc = f % (HD / 16);
+        const int key = c * kRKeys + r;
+        const bool ok = key < len;  // rows past the end arrive as zeros and are not read
+        const uint8_t* src = (is_v ? vbase : kbase) + (size_t)(ok ? key : 0) * width + cc * 16;
+        cp_async16(smem_u32(dst + is_v * kRKeys * HD + row_piece<HD>(r, cc)), src, ok ? 16 : 0);
+      }
+      if (lane < 2) {
+        const size_t j = (size_t)((c * kRKeys) >> p.block_log2) * p.n_kv;
+        cp_async4(smem_u32(dst + 2 * kRKeys * HD + 4 * lane), (lane ? vsc : ksc) + j);
+      }
+    }
+    cp_async_commit();
+  };
+
+  float o[VB][4];
+#pragma unroll
+  for (int j = 0; j < VB; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+  int cf = c0 + warp;
+#pragma unroll
+  for (int st = 0; st < kRStages - 1; ++st, cf += kRWarps) fetch(cf, st);
+  int st = 0;
+  for (int c = c0 + warp; c < c1; c += kRWarps) {
+    cp_async_wait<kRStages - 2>();
+    __syncwarp();
+    fetch(cf, (st + kRStages - 1) % kRStages);
+    cf += kRWarps;
+    const uint8_t* sk = ring + st * SB;
+    const uint8_t* sv = sk + kRKeys * HD;
+    const float2 sc = *reinterpret_cast<const float2*>(sk + 2 * kRKeys * HD);
+    st = (st + 1) % kRStages;
+
+    // S = Q K^T, two n8 tiles of keys
+    float s[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+      uint32_t kw[KW];
+      if constexpr (HD == 128) {
+        uint32_t w0[4], w1[4];
+        lds_words<16>(w0, sk + row_piece<HD>(t * 8 + g, tig * 2));
+        lds_words<16>(w1, sk + row_piece<HD>(t * 8 + g, tig * 2 + 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { kw[i] = w0[i]; kw[4 + i] = w1[i]; }
+      } else if constexpr (HD == 64) {
+        lds_words<16>(kw, sk + row_piece<HD>(t * 8 + g, tig));
+      } else {
+        lds_words<8>(kw, sk + row_piece<HD>(t * 8 + g, tig >> 1) + (tig & 1) * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        uint32_t b0, b1;
+        q8_word_to_bf16<FMT>(kw[i], b0, b1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_bf16(s[t], q[n][i], b0, b1);
+      }
+    }
+    // scores in units of log2, keys past the end out
+    const float ks = sc.x * p.scale_log2;
+    const int key0 = c * kRKeys + tig * 2;
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[t][e] = key0 + t * 8 + (e & 1) < len ? s[t][e] * ks : -INFINITY;
+        mx[e >> 1] = fmaxf(mx[e >> 1], s[t][e]);
+      }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+      mx[i] = fmaxf(mx[i], m[i]);
+    }
+    if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+      const float f0 = exp2f(m[0] - mx[0]), f1 = exp2f(m[1] - mx[1]);
+      l[0] *= f0;
+      l[1] *= f1;
+#pragma unroll
+      for (int j = 0; j < VB; ++j) {
+        o[j][0] *= f0; o[j][1] *= f0;
+        o[j][2] *= f1; o[j][3] *= f1;
+      }
+      m[0] = mx[0];
+      m[1] = mx[1];
+    }
+    uint32_t pa[NT][4];
+    {
+      float pr[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pr[t][e] = exp2f(s[t][e] - m[e >> 1]);
+          l[e >> 1] += pr[t][e];
+          pr[t][e] *= sc.y;
+        }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        pa[n][0] = split_bf16(pr[0][0], pr[0][1]);
+        pa[n][1] = split_bf16(pr[0][2], pr[0][3]);
+        pa[n][2] = split_bf16(pr[1][0], pr[1][1]);
+        pa[n][3] = split_bf16(pr[1][2], pr[1][3]);
+      }
+    }
+    // O += P V: keys 2 tig, 2 tig + 1 and those + 8; columns g * VB ..
+    uint32_t vw[4][VB / 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = tig * 2 + (i & 1) + (i >> 1) * 8;
+      lds_words<VB>(vw[i], sv + row_piece<HD>(r, g * VB / 16) + (g * VB) % 16);
+    }
+#pragma unroll
+    for (int j = 0; j < VB; ++j) {
+      // bytes j of the two rows at byte positions 0 and 2
+      const uint32_t sel = 0x0400u + (j & 3) * 0x0101u;
+      const uint32_t b0 = q8_to_bf162_lo<FMT>(__byte_perm(vw[0][j >> 2], vw[1][j >> 2], sel));
+      const uint32_t b1 = q8_to_bf162_lo<FMT>(__byte_perm(vw[2][j >> 2], vw[3][j >> 2], sel));
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_bf16(o[j], pa[n], b0, b1);
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+
+  // join the warps: rows of [m, l, O] per warp in shared memory
+  float* jm = reinterpret_cast<float*>(smem);  // [warps][16]
+  float* jl = jm + kRWarps * 16;
+  float* jo = jl + kRWarps * 16;               // [warps][16][HD]
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    if (tig == 0) {
+      jm[warp * 16 + g + 8 * i] = m[i];
+      jl[warp * 16 + g + 8 * i] = l[i];
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int j = 0; j < VB; ++j)
+        jo[(warp * 16 + g + 8 * i) * HD + (tig * 2 + e) * VB + j] = o[j][2 * i + e];
+  }
+  __syncthreads();
+  const int rows = min(16, R - tile * 16);
+  const size_t grp = ((size_t)b * p.n_kv + h) * p.tiles + tile;
+  // a task = 4 columns of one row
+  for (int task = threadIdx.x; task < rows * (HD / 4); task += kRThreads) {
+    const int row = task / (HD / 4), col = (task % (HD / 4)) * 4;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kRWarps; ++w) mm = fmaxf(mm, jm[w * 16 + row]);
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kRWarps; ++w) {
+      const float mw = jm[w * 16 + row], f = mw == -INFINITY ? 0.f : exp2f(mw - mm);
+      L += f * jl[w * 16 + row];
+      const float4 v = *reinterpret_cast<const float4*>(jo + (w * 16 + row) * HD + col);
+      acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
+    }
+    const int r = tile * 16 + row;
+    if (S == 1) {
+      const float inv = L != 0.f ? 1.0f / L : 0.f;  // no key: zeros
+      T* dst = reinterpret_cast<T*>(p.O) +
+               (((size_t)b * p.k + r / p.group) * p.n_heads + (size_t)h * p.group + r % p.group) * HD + col;
+      store4(dst, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    } else {
+      const size_t slot = grp * S + sp;
+      *reinterpret_cast<float4*>(p.part_o + (slot * 16 + row) * HD + col) = acc;
+      if (col == 0) {
+        p.part_ml[(slot * 16 + row) * 2] = mm;
+        p.part_ml[(slot * 16 + row) * 2 + 1] = L;
+      }
+    }
+  }
+  if (S == 1) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = atomicAdd(p.sync + grp, 1) == S - 1;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  for (int task = threadIdx.x; task < rows * (HD / 4); task += kRThreads) {
+    const int row = task / (HD / 4), col = (task % (HD / 4)) * 4;
+    float mm = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < S; ++s) mm = fmaxf(mm, __ldcg(p.part_ml + ((grp * S + s) * 16 + row) * 2));
+#pragma unroll 4
+    for (int s = 0; s < S; ++s) {
+      const size_t pr = (grp * S + s) * 16 + row;
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + pr * 2));
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + pr * HD + col));
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mm);
+      L += f * ml.y;
+      acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
+    }
+    const float inv = L != 0.f ? 1.0f / L : 0.f;
+    const int r = tile * 16 + row;
+    T* dst = reinterpret_cast<T*>(p.O) +
+             (((size_t)b * p.k + r / p.group) * p.n_heads + (size_t)h * p.group + r % p.group) * HD + col;
+    store4(dst, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  }
+  if (threadIdx.x == 0) p.sync[grp] = 0;  // ready for the next launch
+}
+
+template <typename T, int HD, int FMT>
+static cudaError_t launch_rows(const Q8AttnParams& p, cudaStream_t stream) {
+  auto kern = q8_attn_rows_kernel<T, HD, FMT>;
+  const cudaError_t e = configure_kernel((const void*)kern, RowCfg<HD>::kSmem, false);
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, dim3(p.tiles * p.splits, p.n_kv, p.B), dim3(kRThreads), RowCfg<HD>::kSmem, stream, p);
+}
+
+// Key shares of a row tile: enough CTAs to keep about three on each SM (their
+// copies in flight are what reaches the HBM rate), each with at least two
+// chunks per warp, within the scratch.
+static int rows_splits(const Q8AttnParams& p, int hd, int num_sms, size_t part_rows, size_t sync_len) {
+  const long long groups = (long long)p.B * p.n_kv * p.tiles;
+  const int most = p.N / (2 * kRKeys * kRWarps);
+  long long s = 3LL * num_sms / groups;
+  s = s < most ? s : most;
+  s = s < 64 ? s : 64;
+  if (groups > (long long)sync_len) s = 1;
+  const long long fit = (long long)(part_rows / 16) / groups;
+  s = s < fit ? s : fit;
+  return s < 1 ? 1 : (int)s;
+}
+
+cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, float* part, size_t part_floats,
+                                size_t sync_len, int num_sms, cudaStream_t stream) {
+  p.tiles = (p.k * p.group + 15) / 16;
+  const size_t part_rows = part_floats / (hd + 2) / 16 * 16;
+  p.splits = rows_splits(p, hd, num_sms, part_rows, sync_len);
+  p.part_o = part;
+  p.part_ml = part + part_rows * hd;
+#define SPA_Q8_CASE(T_, HD_)                                                            \
+  if (hd == HD_)                                                                        \
+    return fmt == kQ8Int8 ? launch_rows<T_, HD_, kQ8Int8>(p, stream) : launch_rows<T_, HD_, kQ8E4m3>(p, stream);
+  if (dtype == 1) {
+    SPA_Q8_CASE(__nv_bfloat16, 32)
+    SPA_Q8_CASE(__nv_bfloat16, 64)
+    SPA_Q8_CASE(__nv_bfloat16, 128)
+  } else {
+    SPA_Q8_CASE(float, 32)
+    SPA_Q8_CASE(float, 64)
+    SPA_Q8_CASE(float, 128)
+  }
+#undef SPA_Q8_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace spa

@@ -22,6 +22,7 @@ lib = ctypes.CDLL(LIB_PATH)
 
 SPA_OK = 0
 SPA_F32, SPA_BF16 = 0, 1
+SPA_Q8_INT8, SPA_Q8_E4M3 = 0, 1
 STATUS = {0: "SPA_OK", -1: "SPA_ERR_INVALID", -2: "SPA_ERR_SHAPE", -3: "SPA_ERR_CUDA",
           -4: "SPA_ERR_NOMEM", -5: "SPA_ERR_UNSUPPORTED", -6: "SPA_ERR_TIMEOUT",
           -7: "SPA_ERR_DEVICE"}
@@ -37,7 +38,9 @@ EXPORTS = [
     "spa_model_create", "spa_model_free", "spa_model_layer_k", "spa_model_index_set", "spa_model_embed",
     "spa_decode_step", "spa_decode_layers", "spa_decode_confidence", "spa_model_write_tokens",
     "spa_decode_graph_capture", "spa_decode_graph_launch", "spa_decode_graph_kernel_nodes",
-    "spa_model_set_incremental_proxy", "spa_debug_fail_alloc_after", "spa_debug_bounded_wait",
+    "spa_model_set_incremental_proxy",
+    "spa_q8_write", "spa_q8_read", "spa_q8_attention", "spa_layer_step_q8", "spa_full_block_q8", "spa_model_set_q8",
+    "spa_token_logprobs", "spa_decode_logits", "spa_debug_fail_alloc_after", "spa_debug_bounded_wait",
     "spa_attention_noalloc", "spa_attention_noalloc_status",
 ]
 
@@ -69,6 +72,12 @@ class LayerWeights(ctypes.Structure):
 class LayerCacheDesc(ctypes.Structure):
     _fields_ = [("k_cache", c_void_p), ("v_cache", c_void_p), ("h_cache", c_void_p),
                 ("p_cache", c_void_p), ("B", c_int), ("N", c_int)]
+
+
+class Q8CacheDesc(ctypes.Structure):
+    _fields_ = [("k_codes", c_void_p), ("v_codes", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("B", c_int), ("N", c_int), ("n_kv_heads", c_int), ("head_dim", c_int), ("block", c_int),
+                ("format", c_int)]
 
 
 class Intermediates(ctypes.Structure):
@@ -131,6 +140,16 @@ _sig("spa_decode_graph_kernel_nodes", c_int, c_void_p)
 _sig("spa_attention_noalloc", c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int,
      c_int, c_int, c_void_p)
 _sig("spa_attention_noalloc_status", c_int, c_void_p)
+_sig("spa_q8_write", c_int, c_void_p, POINTER(Q8CacheDesc), c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p)
+_sig("spa_q8_read", c_int, c_void_p, POINTER(Q8CacheDesc), c_void_p, c_int, c_void_p, c_void_p, c_void_p)
+_sig("spa_q8_attention", c_int, c_void_p, c_void_p, POINTER(Q8CacheDesc), c_void_p, c_void_p, c_int, c_void_p)
+_sig("spa_layer_step_q8", c_int, c_void_p, c_void_p, POINTER(LayerCacheDesc), POINTER(Q8CacheDesc), c_int, c_void_p,
+     c_void_p)
+_sig("spa_full_block_q8", c_int, c_void_p, c_void_p, POINTER(LayerCacheDesc), POINTER(Q8CacheDesc), c_int, c_void_p)
+_sig("spa_model_set_q8", c_int, c_void_p, POINTER(Q8CacheDesc))
+_sig("spa_token_logprobs", c_int, c_void_p, c_void_p, c_int, ctypes.c_longlong, c_int, ctypes.c_longlong, c_void_p,
+     c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p)
+_sig("spa_decode_logits", c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p)
 _sig("spa_debug_fail_alloc_after", c_int, ctypes.c_longlong)
 _sig("spa_debug_bounded_wait", c_int, c_void_p, c_void_p, c_int, c_double, c_void_p)
 
@@ -361,6 +380,137 @@ class Model:
             self.close()
         except Exception:
             pass
+
+
+# --------------------------------------------------- 8-bit K/V cache, log probabilities
+
+def _arg(t, name: str, shape, dtype, device=None, rows_strided=False):
+    """Checks a tensor argument whose layout the C ABI cannot see."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    n = 1
+    for s in shape:
+        n *= s
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {tuple(shape)}, not {tuple(t.shape)}")
+    if not rows_strided and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+class Q8Cache:
+    """An 8-bit K/V cache (torch-owned, zeroed): codes k, v [B, N, n_kv_heads * head_dim] (int8 or
+    float8_e4m3fn) and scales k_scale, v_scale [B, ceil(N / block), n_kv_heads] float32."""
+
+    def __init__(self, B: int, N: int, n_kv_heads: int, head_dim: int, block: int = 64, fmt: int = SPA_Q8_INT8,
+                 device="cuda"):
+        if fmt not in (SPA_Q8_INT8, SPA_Q8_E4M3):
+            raise ValueError("fmt must be SPA_Q8_INT8 or SPA_Q8_E4M3")
+        if block not in (16, 32, 64, 128):
+            raise ValueError("block must be 16, 32, 64 or 128")
+        code = torch.int8 if fmt == SPA_Q8_INT8 else torch.float8_e4m3fn
+        w = n_kv_heads * head_dim
+        self.k = torch.zeros((B, N, w), dtype=torch.uint8, device=device).view(code)
+        self.v = torch.zeros((B, N, w), dtype=torch.uint8, device=device).view(code)
+        nb = (N + block - 1) // block
+        self.k_scale = torch.zeros((B, nb, n_kv_heads), dtype=torch.float32, device=device)
+        self.v_scale = torch.zeros((B, nb, n_kv_heads), dtype=torch.float32, device=device)
+        self.B, self.N, self.n_kv_heads, self.head_dim, self.block, self.fmt = B, N, n_kv_heads, head_dim, block, fmt
+        self.desc = Q8CacheDesc(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                                self.v_scale.data_ptr(), B, N, n_kv_heads, head_dim, block, fmt)
+
+
+def spa_q8_write(ws: Workspace, cache: Q8Cache, k_rows, v_rows, idx=None, indexed: bool = False, stream=None):
+    """Writes k_rows, v_rows [B, k, n_kv_heads * head_dim] into rows idx [B, k] (None: 0..k-1) of the cache;
+    with indexed, the rows idx of k_rows, v_rows [B, N, n_kv_heads * head_dim]."""
+    dt, dev, w = torch_dtype(ws.desc.dtype), cache.k.device, cache.n_kv_heads * cache.head_dim
+    if idx is not None:
+        k = idx.numel() // cache.B
+        _arg(idx, "idx", (cache.B, k), torch.int32, dev)
+    else:
+        k = cache.N if indexed else k_rows.numel() // (cache.B * w)
+    n = cache.N if indexed else k
+    kp = _arg(k_rows, "k_rows", (cache.B, n, w), dt, dev)
+    vp = _arg(v_rows, "v_rows", (cache.B, n, w), dt, dev)
+    _check(lib.spa_q8_write(ws.handle, ctypes.byref(cache.desc), kp, vp, int(indexed), _ptr(idx), k,
+                            _stream(stream)), "spa_q8_write")
+
+
+def spa_q8_read(ws: Workspace, cache: Q8Cache, k_out, v_out, idx=None, stream=None):
+    """Values of rows idx [B, k] (None: 0..k-1) into k_out, v_out [B, k, n_kv_heads * head_dim]."""
+    dt, dev, w = torch_dtype(ws.desc.dtype), cache.k.device, cache.n_kv_heads * cache.head_dim
+    k = k_out.numel() // (cache.B * w)
+    if idx is not None:
+        _arg(idx, "idx", (cache.B, k), torch.int32, dev)
+    kp = _arg(k_out, "k_out", (cache.B, k, w), dt, dev)
+    vp = _arg(v_out, "v_out", (cache.B, k, w), dt, dev)
+    _check(lib.spa_q8_read(ws.handle, ctypes.byref(cache.desc), _ptr(idx), k, kp, vp, _stream(stream)),
+           "spa_q8_read")
+
+
+def spa_q8_attention(ws: Workspace, Q, cache: Q8Cache, O, lens=None, stream=None):
+    """O = attention of Q [B, k, n_heads * head_dim] over the first lens [B] rows (None: all) of the cache."""
+    dt, dev, d = torch_dtype(ws.desc.dtype), cache.k.device, ws.desc.d
+    k = Q.numel() // (cache.B * d)
+    qp = _arg(Q, "Q", (cache.B, k, d), dt, dev)
+    op = _arg(O, "O", (cache.B, k, d), dt, dev)
+    lp = None if lens is None else _arg(lens, "lens", (cache.B,), torch.int32, dev)
+    _check(lib.spa_q8_attention(ws.handle, qp, ctypes.byref(cache.desc), lp, op, k, _stream(stream)),
+           "spa_q8_attention")
+
+
+def spa_layer_step_q8(layer: Layer, H, cache: Cache, q8: Q8Cache, k: int, idx, stream=None):
+    _check(lib.spa_layer_step_q8(layer.handle, _ptr(H), ctypes.byref(cache.desc), ctypes.byref(q8.desc), k,
+                                 _ptr(idx), _stream(stream)), "spa_layer_step_q8")
+
+
+def spa_full_block_q8(layer: Layer, H, cache: Cache, q8: Q8Cache, fill_proxy: int = 1, stream=None):
+    _check(lib.spa_full_block_q8(layer.handle, _ptr(H), ctypes.byref(cache.desc), ctypes.byref(q8.desc),
+                                 int(fill_proxy), _stream(stream)), "spa_full_block_q8")
+
+
+def spa_model_set_q8(model: Model, caches):
+    """8-bit K/V caches for the model's layers (a list of Q8Cache, kept referenced), or None."""
+    arr = None
+    if caches is not None:
+        if len(caches) != len(model.layers):
+            raise ValueError("one Q8Cache per layer")
+        arr = (Q8CacheDesc * len(caches))(*[c.desc for c in caches])
+    _check(lib.spa_model_set_q8(model.handle, arr), "spa_model_set_q8")
+    model.q8 = caches
+
+
+def spa_token_logprobs(ws: Workspace, logits, tok, logp, entropy, top_id=None, top_logp=None, stream=None):
+    """Log probabilities of tok [rows], entropies and the top alternatives of logits [rows, vocab] (float32 or
+    bfloat16; the last dimension contiguous, any row stride); top_id, top_logp [rows, top] or None."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be a [rows, vocab] float32 or bfloat16 tensor")
+    rows, vocab = logits.shape
+    if rows < 1 or vocab < 1:
+        raise ValueError("logits must not be empty")
+    if (vocab > 1 and logits.stride(1) != 1) or (rows > 1 and logits.stride(0) < vocab):
+        raise ValueError("logits must be contiguous along the vocabulary, with rows that do not overlap")
+    dev = logits.device
+    lp = _arg(logits, "logits", (rows, vocab), logits.dtype, dev, rows_strided=True)
+    top = 0 if top_id is None else top_id.numel() // rows
+    args = [_arg(tok, "tok", (rows,), torch.int32, dev), top, _arg(logp, "logp", (rows,), torch.float32, dev),
+            _arg(entropy, "entropy", (rows,), torch.float32, dev)]
+    if top:
+        args += [_arg(top_id, "top_id", (rows, top), torch.int32, dev),
+                 _arg(top_logp, "top_logp", (rows, top), torch.float32, dev)]
+    else:
+        args += [None, None]
+    _check(lib.spa_token_logprobs(ws.handle, lp, SPA_BF16 if logits.dtype == torch.bfloat16 else SPA_F32, rows, vocab,
+                                  logits.stride(0) if rows > 1 else vocab, *args, _stream(stream)),
+           "spa_token_logprobs")
+
+
+def spa_decode_logits(model: Model, pos, u: int, logits, stream=None):
+    _check(lib.spa_decode_logits(model.handle, _ptr(pos), u, _ptr(logits), _stream(stream)), "spa_decode_logits")
 
 
 def spa_decode_layers(model: Model, full: int, stream=None):

@@ -48,7 +48,7 @@ typedef enum {
   SPA_ERR_NOMEM = -4,       /* device or host allocation failed */
   SPA_ERR_UNSUPPORTED = -5, /* valid, but not built for this configuration */
   SPA_ERR_TIMEOUT = -6,     /* a device-side bounded wait ran out */
-  SPA_ERR_DEVICE = -7       /* a device-side index check failed */
+  SPA_ERR_DEVICE = -7       /* a device-side index or value check failed */
 } spa_status;
 
 enum { SPA_F32 = 0, SPA_BF16 = 1 };
@@ -310,6 +310,96 @@ int spa_decode_graph_kernel_nodes(const spa_model *model);
  * (SPA_ERR_INVALID) once the state has gone stale.  Errors: SPA_ERR_INVALID
  * (null model), SPA_ERR_NOMEM. */
 int spa_model_set_incremental_proxy(spa_model *model, int enable);
+
+/* ------------------------------------------------------ 8-bit K/V cache --
+ * No counterpart on the pages: an engineering addition.  K^c and V^c are the
+ * largest state of a batched decode; held in 8 bits they take half of it.
+ *
+ * A cache holds codes and scales of the keys and values of B sequences of N
+ * tokens (device, caller-owned): codes [B, N, n_kv_heads * head_dim], one
+ * byte each, int8 in -127..127 (SPA_Q8_INT8) or e4m3 (SPA_Q8_E4M3, whose NaN
+ * codes do not occur), 16-byte aligned; scales [B, ceil(N / block),
+ * n_kv_heads] float, one for each `block` tokens of a head (the last block
+ * may be cut by N).  A value is its code times its scale.  Start with all
+ * bytes of the four buffers zero.  head_dim is 32, 64 or 128 and that of the
+ * workspace's layer descriptor; n_kv_heads divides its n_heads (query head h
+ * reads kv head h / (n_heads / n_kv_heads)); rows passed to and from the
+ * calls have the descriptor's dtype. */
+enum { SPA_Q8_INT8 = 0, SPA_Q8_E4M3 = 1 };
+typedef struct {
+  void *k_codes, *v_codes;
+  float *k_scale, *v_scale;
+  int B, N, n_kv_heads, head_dim;
+  int block;  /* tokens per scale: 16, 32, 64 or 128 */
+  int format; /* SPA_Q8_INT8 or SPA_Q8_E4M3 */
+} spa_q8_cache;
+
+/* Writes k rows per sequence into the cache: row idx[b, i] ([B, k] int32
+ * device, any order; NULL: row i) takes k_rows / v_rows row [b, i] of
+ * [B, k, n_kv_heads * head_dim] (indexed = 0), or row [b, idx[b, i]] of
+ * [B, N, n_kv_heads * head_dim] (indexed = 1: the layout of K^c and V^c).  An
+ * index given twice takes the later row; one outside [0, N) is skipped and
+ * reported (SPA_ERR_DEVICE).  Every block that gets a row is given the scale
+ * s, the smallest power of two >= 2^-126 with max |v| <= qmax * s (qmax 127
+ * or 448) over its new rows and its remaining rows' values, 0 if all are 0;
+ * its codes are round(v / s), ties to even, the division exact.  A remaining
+ * row thus keeps its values exactly unless the scale grows.  Blocks without
+ * a new row are not touched.  A NaN or an infinity is stored as 0 and
+ * reported (SPA_ERR_DEVICE).  1 <= k <= N; k_rows and v_rows 16-byte aligned. */
+int spa_q8_write(spa_workspace *ws, const spa_q8_cache *cache, const void *k_rows, const void *v_rows,
+                 int indexed, const int32_t *idx, int k, void *stream);
+/* Reads rows back: k_out / v_out [B, k, n_kv_heads * head_dim] (16-byte
+ * aligned) receive the values of rows idx[b, i] ([B, k] int32 device; NULL:
+ * rows 0..k-1, k <= N), exact in bf16 and fp32 for the scales spa_q8_write
+ * makes.  The output row of an index outside [0, N) is left as it was and
+ * reported. */
+int spa_q8_read(spa_workspace *ws, const spa_q8_cache *cache, const int32_t *idx, int k, void *k_out,
+                void *v_out, void *stream);
+/* O = softmax(Q K^T / sqrt(head_dim)) V over the first lens[b] rows of each
+ * sequence ([B] int32 device; NULL: all N; a value outside [0, N] is clamped
+ * and reported): Q, O [B, k, n_heads * head_dim], the descriptor's dtype,
+ * 16-byte aligned and not overlapping, k >= 1 queries per sequence.  A sequence of length 0 gives zeros.  Cache rows
+ * past the length are not read into the result, whatever they hold.  Scores,
+ * softmax statistics and sums are fp32; with bf16 queries the probabilities
+ * are rounded to bf16 before the product with V, as in spa_partial_block. */
+int spa_q8_attention(spa_workspace *ws, const void *Q, const spa_q8_cache *cache, const int32_t *lens,
+                     void *O, int k, void *stream);
+
+/* spa_layer_step and spa_full_block with an 8-bit K/V cache (B, N of
+ * `cache`, n_kv_heads = n_heads): the fresh K and V rows are staged in
+ * cache->k_cache / v_cache, written from there into q8, and the attention
+ * reads q8.  The staging buffers hold nothing between calls, so the caches of
+ * many layers may share one pair; H^c and P^c are as before. */
+int spa_layer_step_q8(spa_layer *layer, const void *H, const spa_layer_cache *cache, const spa_q8_cache *q8,
+                      int k, int32_t *idx, void *stream);
+int spa_full_block_q8(spa_layer *layer, const void *H, const spa_layer_cache *cache, const spa_q8_cache *q8,
+                      int fill_proxy, void *stream);
+/* Every later step of the model (spa_decode_step, spa_decode_layers, a graph
+ * captured from now on) keeps its keys and values in caches[l] (n_layers
+ * descriptors, copied; their buffers borrowed); NULL goes back to the layers'
+ * own K^c and V^c.  Drops a captured graph.  Follow it with a fill (full = 1). */
+int spa_model_set_q8(spa_model *model, const spa_q8_cache *caches);
+
+/* --------------------------------------------------- token log probabilities --
+ * For each of `rows` rows of logits [rows, vocab] (device, dtype SPA_F32 or
+ * SPA_BF16, row r at logits + r * row_stride elements, row_stride >= vocab):
+ * logp[r] = log softmax(row)[tok[r]] (tok [rows] int32 device; one outside
+ * [0, vocab) gives NaN and is reported), entropy[r] = -sum p log p in nats,
+ * and the `top` (0..32) most likely ids, highest first and the lower id first
+ * on ties, into top_id [rows, top] with their log probabilities in top_logp
+ * [rows, top] (float; both may be NULL for top = 0).  A logit of -inf is a
+ * masked token: its log probability is -inf, and it is no alternative (an
+ * alternative that does not exist has id -1 and -inf).  A row of -inf only
+ * has log probability -inf and entropy 0; a row with a NaN or +inf has NaN
+ * values.  One pass over the logits; statistics in fp32.  The workspace holds
+ * the error word only, so any one will do. */
+int spa_token_logprobs(spa_workspace *ws, const void *logits, int dtype, long long rows, int vocab,
+                       long long row_stride, const int32_t *tok, int top, float *logp, float *entropy,
+                       int32_t *top_id, float *top_logp, void *stream);
+/* The logits behind spa_decode_confidence: final RMSNorm and LM head at u
+ * positions pos ([B, u] int32 device) into logits [B * u, vocab] (float,
+ * device, 16-byte aligned), the LM head's fp32 sums unrounded. */
+int spa_decode_logits(spa_model *model, const int32_t *pos, int u, float *logits, void *stream);
 
 /* ------------------------------------------------------- testing hooks --
  * No counterpart on the pages: hooks that let tests drive the failure paths

@@ -1,0 +1,647 @@
+"""GPU tests of the 8-bit K/V cache: rows written and read back against the
+definition in 64 bits (bit for bit: the scales are powers of two, so every
+quotient is exact), the attention over it against 64-bit softmax attention on
+the same codes, and the layer and decode paths that use it.
+
+Tolerance of the attention, per element, from the roundings it makes.  With
+A = sum_j softmax_j |v_j| (64-bit):
+  - a probability is rounded to bf16 once, 2^-8 relative (fp32: three bf16
+    terms, 2^-24), which moves the result by at most that times A;
+  - the result is rounded to its type, 2^-8 (2^-24) relative;
+  - scores are fp32 sums of hd products (the tensor core may truncate: 2^-23
+    each): an error of ds = (hd + 8) 2^-23 max_j sum_c |q_c k_jc| / sqrt(hd),
+    which moves every softmax weight by at most the factor e^(2 ds);
+  - sums over n keys in fp32: n 2^-23 A, and the exponential's 2^-21.
+"""
+import numpy as np
+import pytest
+import torch
+
+from adaptive_hidden_state_b200 import synth
+from spa_testutil import LayerPair, assert_close, np64
+
+pytestmark = pytest.mark.gpu
+
+spa = pytest.importorskip("adaptive_hidden_state_b200.spa")
+
+INT8, E4M3 = spa.SPA_Q8_INT8, spa.SPA_Q8_E4M3
+BF16, F32 = spa.SPA_BF16, spa.SPA_F32
+QMAX = {INT8: 127.0, E4M3: 448.0}
+
+
+def make_ws(dtype, n_heads, hd, B=1, N=256):
+    d = n_heads * hd
+    return spa.Workspace(spa.LayerDesc(d=d, n_heads=n_heads, head_dim=hd, ffn=128, r=1, dtype=dtype, rms_eps=1e-5,
+                                       rope_theta=1e4), B, N)
+
+
+def heads_for(dtype, kv, hd):
+    """The smallest multiple of kv heads that makes a layer width the descriptor takes."""
+    n = kv
+    while dtype == BF16 and (n * hd) % 256:
+        n += kv
+    return n
+
+
+# ------------------------------------------------------------ 64-bit definition
+
+def ref_scale(A, qmax):
+    if A == 0:
+        return 0.0
+    t = -126
+    e = int(np.floor(np.log2(A / qmax))) - 2
+    t = max(t, e)
+    while A > qmax * 2.0 ** t:
+        t += 1
+    return 2.0 ** t
+
+
+def ref_round(y, fmt):
+    if fmt == INT8:
+        return np.rint(y)
+    a = np.maximum(np.abs(y), 2.0 ** -6)
+    step = 2.0 ** (np.floor(np.log2(a)) - 3)
+    return np.rint(y / step) * step
+
+
+class RefCache:
+    """Values and scales of one of K or V: [B, N, kv, hd] and [B, blocks, kv]."""
+
+    def __init__(self, B, N, kv, hd, block, fmt):
+        self.v = np.zeros((B, N, kv, hd))
+        self.s = np.zeros((B, (N + block - 1) // block, kv))
+        self.block, self.fmt = block, fmt
+
+    def write(self, rows, idx, indexed=False):
+        """rows float64; idx [B, k] (indices outside the cache skipped, a later equal one wins)."""
+        B, N, kv, hd = self.v.shape
+        for b in range(B):
+            hit = set()
+            for i, r in enumerate(idx[b]):
+                if 0 <= r < N:
+                    x = rows[b, r if indexed else i].reshape(kv, hd)
+                    self.v[b, r] = np.where(np.isfinite(x), x, 0.0)
+                    hit.add(int(r) // self.block)
+            for j in hit:
+                sl = slice(j * self.block, min((j + 1) * self.block, N))
+                for h in range(kv):
+                    blk = self.v[b, sl, h]
+                    s = ref_scale(np.abs(blk).max(), QMAX[self.fmt])
+                    self.s[b, j, h] = s
+                    if s:
+                        self.v[b, sl, h] = ref_round(blk / s, self.fmt) * s
+
+
+def device_values(cache, which):
+    """[B, N, kv, hd] float64 values of a device cache from its own codes and scales."""
+    codes = (cache.k if which == "k" else cache.v).float().cpu().numpy().astype(np.float64)
+    s = (cache.k_scale if which == "k" else cache.v_scale).cpu().numpy().astype(np.float64)
+    s = np.repeat(s, cache.block, axis=1)[:, :cache.N]
+    return codes.reshape(cache.B, cache.N, cache.n_kv_heads, cache.head_dim) * s[..., None], s
+
+
+def check_cache(cache, ref_k, ref_v, what):
+    for which, ref in (("k", ref_k), ("v", ref_v)):
+        v, _ = device_values(cache, which)
+        sc = (cache.k_scale if which == "k" else cache.v_scale).cpu().numpy()
+        assert np.array_equal(sc, ref.s), f"{what}: {which} scales"
+        assert np.array_equal(v, ref.v), f"{what}: {which} values"
+
+
+def rows_of(rng, shape, dtype, spread=1.0):
+    x = rng.standard_normal(shape) * np.exp(spread * rng.standard_normal(shape[:2] + (1,)))
+    t = torch.from_numpy(x.astype(np.float32)).to(spa.torch_dtype(dtype))
+    return t.cuda(), t.float().numpy().astype(np.float64)
+
+
+# ------------------------------------------------------------ write and read
+
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,N,kv,hd,block", [(1, 1, 1, 128, 16), (2, 71, 3, 64, 16), (1, 130, 2, 32, 128),
+                                             (3, 257, 4, 128, 64), (2, 96, 2, 64, 32)])
+def test_writes_follow_the_definition_over_steps(fmt, dtype, B, N, kv, hd, block):
+    rng = np.random.default_rng(N * 7 + hd + fmt)
+    ws = make_ws(dtype, heads_for(dtype, kv, hd), hd, B, N)
+    cache = spa.Q8Cache(B, N, kv, hd, block=block, fmt=fmt)
+    rk, rv = (RefCache(B, N, kv, hd, block, fmt) for _ in range(2))
+    w = kv * hd
+    # some rows of an empty cache, all rows, then steps of rows larger and smaller than what is there
+    for step, (frac, size) in enumerate([(0.3, 1.0), (1.0, 0.5), (0.2, 30.0), (0.4, 1e-3), (0.1, 1e4), (0.5, 1e-30)]):
+        k = max(1, int(frac * N))
+        idx = np.stack([np.sort(rng.permutation(N)[:k]) for _ in range(B)]).astype(np.int32)
+        kr, kr64 = rows_of(rng, (B, k, w), dtype)
+        vr, vr64 = rows_of(rng, (B, k, w), dtype, 2.0)
+        kr, kr64 = (kr * size).to(kr.dtype), None
+        kr64 = np64(kr)
+        use_idx = None if k == N else torch.from_numpy(idx).cuda()
+        spa.spa_q8_write(ws, cache, kr, vr, idx=use_idx)
+        rk.write(kr64, idx)
+        rv.write(vr64, idx)
+        ws.check()
+        check_cache(cache, rk, rv, f"step {step}")
+    for idx in (None, np.stack([rng.integers(0, N, N + 3) for _ in range(B)]).astype(np.int32)):
+        n = N if idx is None else N + 3
+        out = [torch.full((B, n, w), float("nan"), dtype=spa.torch_dtype(dtype), device="cuda") for _ in range(2)]
+        spa.spa_q8_read(ws, cache, out[0], out[1], idx=None if idx is None else torch.from_numpy(idx).cuda())
+        ws.check()
+        for o, r in zip(out, (rk, rv)):
+            want = r.v.reshape(B, N, w)
+            if idx is not None:
+                want = np.stack([want[b][idx[b]] for b in range(B)])
+            # values of normal size are exact in either type
+            if dtype == F32:
+                assert np.array_equal(np64(o), want.astype(np.float32))
+            else:
+                assert np.array_equal(np64(o), np64(torch.from_numpy(want.astype(np.float32)).to(torch.bfloat16)))
+
+
+def test_indexed_rows_come_from_the_full_layout():
+    rng = np.random.default_rng(3)
+    B, N, kv, hd = 2, 100, 2, 128
+    ws = make_ws(BF16, 2, hd, B, N)
+    cache = spa.Q8Cache(B, N, kv, hd, block=32, fmt=INT8)
+    rk, rv = (RefCache(B, N, kv, hd, 32, INT8) for _ in range(2))
+    k_all, k64 = rows_of(rng, (B, N, kv * hd), BF16)
+    v_all, v64 = rows_of(rng, (B, N, kv * hd), BF16)
+    idx = np.stack([rng.permutation(N)[:17] for _ in range(B)]).astype(np.int32)   # any order
+    spa.spa_q8_write(ws, cache, k_all, v_all, idx=torch.from_numpy(idx).cuda(), indexed=True)
+    rk.write(k64, idx, indexed=True)
+    rv.write(v64, idx, indexed=True)
+    ws.check()
+    check_cache(cache, rk, rv, "indexed")
+    spa.spa_q8_write(ws, cache, k_all, v_all, indexed=True)   # every row
+    every = np.tile(np.arange(N), (B, 1))
+    rk.write(k64, every)
+    rv.write(v64, every)
+    check_cache(cache, rk, rv, "every row")
+
+
+def test_equal_and_outside_indices():
+    rng = np.random.default_rng(4)
+    B, N, kv, hd = 2, 70, 1, 64
+    ws = make_ws(F32, 1, hd, B, N)
+    cache = spa.Q8Cache(B, N, kv, hd, block=16, fmt=E4M3)
+    rk, rv = (RefCache(B, N, kv, hd, 16, E4M3) for _ in range(2))
+    idx = np.array([[5, 3, 5, 69, 5], [70, 0, -1, 0, 2 ** 31 - 1]], dtype=np.int32)
+    kr, k64 = rows_of(rng, (B, 5, hd), F32)
+    vr, v64 = rows_of(rng, (B, 5, hd), F32)
+    spa.spa_q8_write(ws, cache, kr, vr, idx=torch.from_numpy(idx).cuda())
+    assert ws.status() == -7   # the outside ones are reported
+    rk.write(k64, idx)
+    rv.write(v64, idx)
+    check_cache(cache, rk, rv, "equal indices")
+    assert ws.status() == 0
+    out = [torch.full((B, 5, hd), 7.0, device="cuda") for _ in range(2)]
+    spa.spa_q8_read(ws, cache, out[0], out[1], idx=torch.from_numpy(idx).cuda())
+    assert ws.status() == -7
+    got = np64(out[0])
+    for b in range(B):
+        for i, r in enumerate(idx[b]):
+            want = rk.v[b, r].reshape(-1) if 0 <= r < N else np.full(hd, 7.0)
+            assert np.array_equal(got[b, i], want)
+
+
+def test_values_a_cache_cannot_hold_are_reported():
+    B, N, kv, hd = 1, 40, 1, 64
+    ws = make_ws(F32, 1, hd, B, N)
+    for fmt in (INT8, E4M3):
+        cache = spa.Q8Cache(B, N, kv, hd, block=16, fmt=fmt)
+        rk, rv = (RefCache(B, N, kv, hd, 16, fmt) for _ in range(2))
+        x = np.random.default_rng(5).standard_normal((B, N, hd)).astype(np.float32)
+        x[0, 0, 3], x[0, 1, 4], x[0, 33, 5] = np.nan, np.inf, -np.inf
+        x[0, 34:] = np.inf                      # whole rows
+        x[0, 16:32] = 0.0                       # a block of zeros
+        x[0, 2, 0], x[0, 3, 0] = 3.4028235e38, -1e-45   # the largest and the smallest that are held (or round to 0)
+        spa.spa_q8_write(ws, cache, torch.from_numpy(x).cuda(), torch.from_numpy(x).cuda())
+        assert ws.status() == -7
+        rk.write(x.astype(np.float64), np.arange(N)[None])
+        rv.write(x.astype(np.float64), np.arange(N)[None])
+        check_cache(cache, rk, rv, f"format {fmt}")
+        assert cache.k_scale[0, 1, 0] == 0
+        # tiny values only: the smallest scale, codes that round to zero or to subnormal codes
+        t = np.full((B, 16, hd), 1e-44, np.float32)
+        t[0, 0] = 2.0 ** -130
+        spa.spa_q8_write(ws, cache, torch.from_numpy(t).cuda(), torch.from_numpy(t).cuda())
+        assert ws.status() == 0
+        rk.write(t.astype(np.float64), np.arange(16)[None])
+        rv.write(t.astype(np.float64), np.arange(16)[None])
+        check_cache(cache, rk, rv, f"format {fmt} tiny")
+
+
+def test_writing_the_same_rows_again_changes_nothing():
+    rng = np.random.default_rng(6)
+    B, N, kv, hd = 2, 200, 2, 128
+    ws = make_ws(BF16, 2, hd, B, N)
+    cache = spa.Q8Cache(B, N, kv, hd, block=64, fmt=INT8)
+    all_k, _ = rows_of(rng, (B, N, kv * hd), BF16, 2.0)
+    spa.spa_q8_write(ws, cache, all_k, all_k)
+    idx = torch.from_numpy(np.stack([np.sort(rng.permutation(N)[:9]) for _ in range(B)]).astype(np.int32)).cuda()
+    rows, _ = rows_of(rng, (B, 9, kv * hd), BF16, 2.0)
+    spa.spa_q8_write(ws, cache, rows, rows, idx=idx)
+    once = [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    spa.spa_q8_write(ws, cache, rows, rows, idx=idx)
+    for a, t in zip(once, (cache.k, cache.v, cache.k_scale, cache.v_scale)):
+        assert torch.equal(a, t)
+
+
+# ------------------------------------------------------------ attention
+
+def fill_cache(rng, cache):
+    """Codes and scales of every kind a cache can hold, blocks of zeros among them."""
+    for codes, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        if cache.fmt == INT8:
+            c = torch.from_numpy(np.clip(np.rint(40 * rng.standard_normal(codes.shape)), -127, 127).astype(np.int8))
+        else:
+            c = torch.from_numpy((100 * rng.standard_normal(codes.shape)).clip(-448, 448).astype(np.float32))
+            c = c.to(torch.float8_e4m3fn)
+        codes.copy_(c.cuda())
+        s = 2.0 ** rng.integers(-8, -5, scale.shape)
+        s[rng.random(scale.shape) < 0.1] = 0.0
+        scale.copy_(torch.from_numpy(s.astype(np.float32)).cuda())
+
+
+def ref_attention(q, cache, lens, n_heads, f32):
+    """q [B, k, n_heads, hd] float64 -> (o, elementwise bound on the kernel's error)."""
+    K, _ = device_values(cache, "k")
+    V, _ = device_values(cache, "v")
+    B, k, _, hd = q.shape
+    group = n_heads // cache.n_kv_heads
+    o, bound = np.zeros_like(q), np.zeros_like(q)
+    r = 2.0 ** -24 if f32 else 2.0 ** -8
+    for b in range(B):
+        n = int(lens[b])
+        if n == 0:
+            continue
+        for h in range(n_heads):
+            Kh, Vh = K[b, :n, h // group], V[b, :n, h // group]
+            s = q[b, :, h] @ Kh.T / np.sqrt(hd)
+            p = np.exp(s - s.max(-1, keepdims=True))
+            p /= p.sum(-1, keepdims=True)
+            o[b, :, h] = p @ Vh
+            A = p @ np.abs(Vh)
+            ds = (hd + 8) * 2.0 ** -23 * (np.abs(q[b, :, h]) @ np.abs(Kh).T).max(-1, keepdims=True) / np.sqrt(hd)
+            bound[b, :, h] = (r + 2.0 ** -21 + n * 2.0 ** -23 + np.expm1(2 * ds)) * A + r * np.abs(o[b, :, h])
+    return o, 1.01 * bound + 1e-37
+
+
+def run_attention(ws, cache, q, lens=None, stream=None):
+    out = torch.full_like(q, float("nan"))
+    spa.spa_q8_attention(ws, q, cache, out, lens=lens, stream=stream)
+    return out
+
+
+def check_attention(dtype, fmt, B, N, heads, kv, hd, k, block, lens, seed, ws=None):
+    rng = np.random.default_rng(seed)
+    ws = ws or make_ws(dtype, heads, hd, B, min(N, 512))
+    cache = spa.Q8Cache(B, N, kv, hd, block=block, fmt=fmt)
+    fill_cache(rng, cache)
+    q = torch.from_numpy(rng.standard_normal((B, k, heads, hd)).astype(np.float32)).to(spa.torch_dtype(dtype)).cuda()
+    ln = [N] * B if lens is None else lens
+    out = run_attention(ws, cache, q, None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    ws.check()
+    ref, bound = ref_attention(np64(q), cache, ln, heads, dtype == F32)
+    err = np.abs(np64(out) - ref)
+    assert np.all(err <= bound), f"worst ratio {np.max(err / bound):.3g}"
+    return out
+
+
+SHAPES = [
+    # B, N, heads, kv, hd, k, block, lens
+    (1, 1, 2, 2, 128, 1, 16, None),
+    (1, 7, 2, 2, 128, 3, 16, None),
+    (2, 16, 4, 2, 64, 1, 16, None),
+    (1, 17, 8, 1, 32, 5, 32, None),
+    (2, 129, 4, 4, 64, 16, 128, None),
+    (1, 300, 2, 2, 128, 17, 64, None),
+    (1, 512, 2, 2, 128, 128, 64, None),
+    (2, 257, 2, 2, 128, 129, 32, None),
+    (1, 640, 4, 1, 128, 70, 128, None),
+    (1, 1000, 14, 2, 128, 1, 16, None),
+    (1, 1000, 14, 2, 128, 40, 16, None),
+    (5, 333, 8, 2, 64, 61, 32, [333, 0, 1, 200, 332]),
+    (4, 200, 2, 2, 128, 150, 64, [0, 0, 128, 129]),
+    (4, 2100, 4, 2, 64, 2, 64, [0, 2100, 1, 1024]),
+    (1, 5000, 2, 1, 128, 1, 128, None),
+    (3, 1100, 2, 2, 128, 300, 64, [1100, 1, 700]),
+    (2, 1024, 8, 8, 32, 33, 64, None),
+]
+
+
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_attention_bf16(fmt, shape):
+    B, N, heads, kv, hd, k, block, lens = shape
+    if heads * hd % 256:
+        heads, kv = 2 * heads, 2 * kv
+    check_attention(BF16, fmt, B, N, heads, kv, hd, k, block, lens, seed=N + k)
+
+
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[1] * s[5] <= 40000])
+def test_attention_f32(fmt, shape):
+    B, N, heads, kv, hd, k, block, lens = shape
+    check_attention(F32, fmt, B, N, heads, kv, hd, k, block, lens, seed=N + k)
+
+
+@pytest.mark.parametrize("hd,k", [(128, 1), (128, 200), (64, 140)])
+def test_attention_ignores_what_lies_past_the_length(hd, k):
+    """NaN scales and codes behind a sequence's rows (and in the next sequences') do not reach its result."""
+    rng = np.random.default_rng(8)
+    B, N, heads = 3, 400, 4
+    ws = make_ws(BF16, heads, hd, B, N)
+    cache = spa.Q8Cache(B, N, heads, hd, block=32, fmt=E4M3)
+    fill_cache(rng, cache)
+    lens = [170, 64, 0]
+    q = torch.from_numpy(rng.standard_normal((B, k, heads, hd)).astype(np.float32)).to(torch.bfloat16).cuda()
+    ld = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    clean = run_attention(ws, cache, q, ld)
+    for b, n in enumerate(lens):
+        cache.k.view(torch.uint8)[b, n:] = 0x7F
+        cache.v.view(torch.uint8)[b, n:] = 0xFF
+        j = (n + 31) // 32
+        cache.k_scale[b, j:] = float("nan")
+        cache.v_scale[b, j:] = float("inf")
+    dirty = run_attention(ws, cache, q, ld)
+    ws.check()
+    assert torch.equal(clean, dirty)
+    assert torch.count_nonzero(clean[2]) == 0
+
+
+def test_attention_lengths_outside_are_clamped_and_reported():
+    rng = np.random.default_rng(9)
+    ws = make_ws(BF16, 2, 128, 2, 64)
+    cache = spa.Q8Cache(2, 50, 2, 128, block=16, fmt=INT8)
+    fill_cache(rng, cache)
+    q = torch.randn((2, 3, 2, 128), device="cuda").to(torch.bfloat16)
+    want = run_attention(ws, cache, q, torch.tensor([50, 0], dtype=torch.int32, device="cuda"))
+    got = run_attention(ws, cache, q, torch.tensor([51, -4], dtype=torch.int32, device="cuda"))
+    assert ws.status() == -7
+    assert torch.equal(want, got)
+
+
+@pytest.mark.parametrize("k", [1, 130])
+def test_attention_nan_query_stays_in_its_row(k):
+    rng = np.random.default_rng(10)
+    ws = make_ws(BF16, 2, 128, 1, 600)
+    cache = spa.Q8Cache(1, 600, 2, 128, block=64, fmt=INT8)
+    fill_cache(rng, cache)
+    q = torch.randn((1, k, 2, 128), device="cuda").to(torch.bfloat16)
+    want = run_attention(ws, cache, q)
+    bad = q.clone()
+    bad[0, k // 2, 1, 5] = float("nan")
+    got = run_attention(ws, cache, bad)
+    assert torch.isnan(got[0, k // 2, 1]).all()
+    keep = torch.ones((1, k, 2), dtype=torch.bool, device="cuda")
+    keep[0, k // 2, 1] = False
+    assert torch.equal(got[keep], want[keep])
+
+
+@pytest.mark.parametrize("k,N", [(1, 3000), (40, 900), (256, 700)])
+def test_attention_repeats_and_streams_and_graphs(k, N):
+    """The same bits on every run, on another stream, and from a replayed graph; two workspaces do not meet."""
+    rng = np.random.default_rng(11)
+    heads, hd = 4, 128
+    ws, ws2 = make_ws(BF16, heads, hd, 2, 1024), make_ws(BF16, heads, hd, 2, 1024)
+    cache = spa.Q8Cache(2, N, 2, hd, block=64, fmt=E4M3)
+    fill_cache(rng, cache)
+    q = torch.randn((2, k, heads, hd), device="cuda").to(torch.bfloat16)
+    want = run_attention(ws, cache, q)
+    for _ in range(3):
+        assert torch.equal(run_attention(ws, cache, q), want)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    o1, o2 = torch.zeros_like(q), torch.zeros_like(q)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        spa.spa_q8_attention(ws, q, cache, o1, stream=s1)
+        spa.spa_q8_attention(ws2, q, cache, o2, stream=s2)
+    torch.cuda.synchronize()
+    assert torch.equal(o1, want) and torch.equal(o2, want)
+    idx = torch.from_numpy(np.stack([np.sort(rng.permutation(N)[:20]) for _ in range(2)]).astype(np.int32)).cuda()
+    kr = torch.randn((2, 20, 2 * hd), device="cuda").to(torch.bfloat16)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s1):
+        spa.spa_q8_attention(ws, q, cache, o1)
+        s1.synchronize()
+        with torch.cuda.graph(g, stream=s1):
+            spa.spa_q8_write(ws, cache, kr, kr, idx=idx)
+            spa.spa_q8_attention(ws, q, cache, o1)
+    for step in range(3):
+        kr.copy_(torch.randn((2, 20, 2 * hd), device="cuda").to(torch.bfloat16))
+        before = [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+        g.replay()
+        torch.cuda.synchronize()
+        after = [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+        for t, b in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), before):
+            t.copy_(b)
+        spa.spa_q8_write(ws2, cache, kr, kr, idx=idx)
+        o2 = run_attention(ws2, cache, q)
+        for t, a in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), after):
+            assert torch.equal(t.view(torch.uint8), a.view(torch.uint8)), f"replay {step}"
+        assert torch.equal(o1, o2), f"replay {step}"
+    ws.check()
+    ws2.check()
+
+
+def test_attention_over_a_cache_past_32_bit_offsets():
+    """More than 2^31 codes: the last sequence's rows lie past any 32-bit offset."""
+    B, N, kv, hd = 3, 1 << 20, 8, 128
+    ws = make_ws(BF16, 8, hd, B, 8192)
+    cache = spa.Q8Cache(B, N, kv, hd, block=128, fmt=INT8)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n = 300
+    tail = torch.randint(-127, 128, (n, kv * hd), generator=g, device="cuda", dtype=torch.int32).to(torch.int8)
+    small = spa.Q8Cache(1, N, kv, hd, block=128, fmt=INT8)
+    for c, b in ((cache, B - 1), (small, 0)):
+        c.k[b, N - n:] = tail
+        c.v[b, N - n:] = tail.flip(0)
+        c.k_scale[b].fill_(2.0 ** -7)
+        c.v_scale[b].fill_(2.0 ** -7)
+    q = torch.randn((B, 1, 8, hd), generator=g, device="cuda").to(torch.bfloat16)
+    out = run_attention(ws, cache, q)
+    ws.check()
+    K = small.k[0, N - n:].double().view(n, kv, hd) * 2.0 ** -7
+    V = small.v[0, N - n:].double().view(n, kv, hd) * 2.0 ** -7
+    s = torch.einsum("hc,nhc->hn", q[B - 1, 0].double(), K) / hd ** 0.5
+    m = torch.clamp(s.amax(-1, keepdim=True), min=0.0)
+    p = torch.exp(s - m)
+    den = p.sum(-1, keepdim=True) + (N - n) * torch.exp(-m)     # the zero keys score 0
+    ref = torch.einsum("hn,nhc->hc", p / den, V)
+    A = torch.einsum("hn,nhc->hc", p / den, V.abs())
+    # 300 keys carry V; the sum of 2^20 weights is split over shares, warps and lanes: runs of at most
+    # 2^20 / (32 shares x 4 warps x 4 keys a lane) additions
+    bound = (2.0 ** -8 + (2048 + n) * 2.0 ** -23 + 1e-4) * A + 2.0 ** -8 * ref.abs()
+    assert torch.all((out[B - 1, 0].double() - ref).abs() <= bound)
+
+
+# ------------------------------------------------------------ layer and decode paths
+
+SHAPE = synth.LayerShape(d=256, n_heads=2, head_dim=128, ffn=384, r=16)
+
+
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dtype,shape", [(BF16, SHAPE), (F32, synth.TINY_LAYER)])
+def test_layer_step_with_an_8_bit_cache(fmt, dtype, shape):
+    """Fill and cached step: the attention output is that of the 8-bit cache's values, the rest of the block
+    follows from it, and the index set and P^c are those of the step without it."""
+    B, N, k = 2, 150, 40
+    lp = LayerPair(spa, shape, seed=81, dtype=dtype, max_B=B, max_N=N, std=0.05)
+    bf = dtype == BF16
+    H = synth.hidden_states(B, N, shape.d, seed=82, bf16=bf)
+    H2, _ = synth.drift_rows(H, 0.2, 0.5, seed=83, bf16=bf)
+    plain, c = lp.cache(B, N), lp.cache(B, N)
+    q8 = spa.Q8Cache(B, N, shape.n_heads, shape.head_dim, block=64, fmt=fmt)
+    rk, rv = (RefCache(B, N, shape.n_heads, shape.head_dim, 64, fmt) for _ in range(2))
+    i1, i2 = (torch.empty((B, k), dtype=torch.int32, device="cuda") for _ in range(2))
+    spa.spa_full_block(lp.layer, lp.to_dev(H), plain, True)
+    spa.spa_layer_step(lp.layer, lp.to_dev(H2), plain, k, i1)
+    lp.ws.check()
+    spa.spa_full_block_q8(lp.layer, lp.to_dev(H), c, q8, True)
+    lp.ws.check()
+    every = np.tile(np.arange(N), (B, 1))
+    rk.write(np64(c.k), every)
+    rv.write(np64(c.v), every)
+    check_cache(q8, rk, rv, "fill")
+    spa.spa_layer_step_q8(lp.layer, lp.to_dev(H2), c, q8, k, i2)
+    lp.ws.check()
+    idx = i2.cpu().numpy()
+    assert torch.equal(i1, i2) and torch.equal(plain.p, c.p)
+    rk.write(np64(c.k), idx, indexed=True)
+    rv.write(np64(c.v), idx, indexed=True)
+    check_cache(q8, rk, rv, "step")
+    M, d = B * k, shape.d
+    tdt = spa.torch_dtype(dtype)
+    q, o, h1 = (lp.ws.view(n, (M, d), tdt).clone() for n in ("q", "o", "h1"))
+    ref, bound = ref_attention(np64(q).reshape(B, k, shape.n_heads, shape.head_dim), q8, [N] * B, shape.n_heads, not bf)
+    assert np.all(np.abs(np64(o).reshape(ref.shape) - ref) <= bound)
+    Hsel = np.concatenate([np64(lp.to_dev(H2)[b])[idx[b]] for b in range(B)])
+    h1_ref = Hsel + np64(o) @ np64(lp.dev["wo"]).T
+    assert_close(h1, h1_ref, bf, "H1")
+    x2 = h1_ref / np.sqrt((h1_ref ** 2).mean(-1, keepdims=True) + shape.rms_eps) * np64(lp.dev["ffn_norm"])
+    gate, up = x2 @ np64(lp.dev["w_gate"]).T, x2 @ np64(lp.dev["w_up"]).T
+    h_ref = h1_ref + (gate / (1 + np.exp(-gate)) * up) @ np64(lp.dev["w_down"]).T
+    got = np.concatenate([np64(c.h[b])[idx[b]] for b in range(B)])
+    assert_close(got, h_ref, bf, "H^c rows")
+
+
+@pytest.mark.parametrize("inc", [False, True])
+def test_decode_over_8_bit_caches_with_log_probabilities(inc):
+    """The operators together, as a decode uses them: a model on 8-bit caches whose layers share one pair of
+    staging buffers; its logits, their log probabilities, entropies and alternatives; a replayed graph."""
+    B, N, L, vocab, u = 2, 96, 3, 1003, 5
+    shape = SHAPE
+    rng = np.random.default_rng(91)
+    lps, ws = [], None
+    for l in range(L):
+        lp = LayerPair(spa, shape, seed=92 + l, dtype=BF16, max_B=B, max_N=N, ws=ws, std=0.05)
+        ws = lp.ws
+        lps.append(lp)
+    dev = lambda a: torch.from_numpy(a.astype(np.float32)).to("cuda", torch.bfloat16)
+    embed, lm, fn = dev(rng.standard_normal((vocab, shape.d))), dev(rng.standard_normal((vocab, shape.d)) * 0.2), dev(np.ones(shape.d))
+    toks = torch.from_numpy(rng.integers(0, vocab, (B, N)).astype(np.int32)).cuda()
+    steps = [torch.from_numpy(np.stack([np.sort(rng.permutation(N)[:u]) for _ in range(B)]).astype(np.int32)).cuda()
+             for _ in range(4)]
+
+    def build():
+        stage = lps[0].cache(B, N)
+        caches = []
+        for lp in lps:
+            c = lp.cache(B, N)
+            c.k, c.v = stage.k, stage.v
+            c.desc.k_cache, c.desc.v_cache = stage.k.data_ptr(), stage.v.data_ptr()
+            caches.append(c)
+        h0 = torch.zeros((B, N, shape.d), dtype=torch.bfloat16, device="cuda")
+        model = spa.Model([lp.layer for lp in lps], caches, h0, embed, fn, lm, vocab, B, N, rho_p=0.25, l_p=1,
+                          rho_1=0.25, rho_L=0.25)
+        q8 = [spa.Q8Cache(B, N, shape.n_heads, shape.head_dim, block=32, fmt=f) for f in (INT8, E4M3, INT8)]
+        spa.spa_model_set_q8(model, q8)
+        model.set_incremental_proxy(inc)
+        model.embed_tokens(toks)
+        return model, caches, q8
+
+    outs = []
+    for use_graph in (False, True):
+        model, caches, q8 = build()
+        tok = torch.empty((B, u), dtype=torch.int32, device="cuda")
+        pos = steps[0].clone()
+        spa.spa_decode_step(model, pos, None, u, 1, tok)
+        stream = torch.cuda.Stream()
+        if use_graph:
+            pos.copy_(steps[1])
+            spa.spa_decode_step(model, pos, None, u, 0, tok)   # a first cached step outside the graph
+            torch.cuda.synchronize()
+            spa.spa_decode_graph_capture(model, pos, None, u, tok, stream=stream)
+        for t in range(1, 4):
+            pos.copy_(steps[t])
+            torch.cuda.synchronize()
+            if use_graph and t > 1:
+                spa.spa_decode_graph_launch(model, stream=stream)
+            elif not use_graph:
+                spa.spa_decode_step(model, pos, None, u, 0, tok, stream=stream)
+            torch.cuda.synchronize()
+        ws.check()
+        outs.append([tok.clone()] + [c.h.clone() for c in caches] + [q.k.view(torch.uint8).clone() for q in q8] +
+                    [q.v_scale.clone() for q in q8])
+        if not use_graph:
+            # log probabilities of the answers
+            conf, t2 = torch.empty((B, u), device="cuda"), torch.empty((B, u), dtype=torch.int32, device="cuda")
+            spa.spa_decode_confidence(model, pos, u, t2, conf)
+            logits = torch.empty((B * u, vocab), device="cuda")
+            spa.spa_decode_logits(model, pos, u, logits)
+            lp_, ent = torch.empty((B * u,), device="cuda"), torch.empty((B * u,), device="cuda")
+            tid = torch.empty((B * u, 4), dtype=torch.int32, device="cuda")
+            tlp = torch.empty((B * u, 4), device="cuda")
+            spa.spa_token_logprobs(ws, logits, t2, lp_, ent, tid, tlp)
+            ws.check()
+            rows = np.concatenate([np64(caches[-1].h[b])[pos[b].cpu().numpy()] for b in range(B)])
+            x = rows / np.sqrt((rows ** 2).mean(-1, keepdims=True) + shape.rms_eps)
+            x = np64(torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16))
+            assert_close(logits, x @ np64(lm).T, True, "logits")
+            assert torch.equal(tid[:, 0].view(B, u), t2) and torch.equal(tlp[:, 0], lp_)
+            assert torch.allclose(tlp[:, 0].exp().view(B, u), conf, rtol=1e-4)
+            ref = torch.log_softmax(logits.double(), -1)
+            assert torch.allclose(ent.double(), -(ref.exp() * ref).sum(-1), rtol=1e-5, atol=1e-6)
+            # the same bits for more than 256 positions (the other product kernel) is not promised; the ids are
+            many = torch.arange(N, dtype=torch.int32, device="cuda").repeat(B, 1)
+            lg = torch.empty((B * N, vocab), device="cuda")
+            spa.spa_decode_logits(model, many, N, lg)
+            tt, cc = torch.empty((B, N), dtype=torch.int32, device="cuda"), torch.empty((B, N), device="cuda")
+            spa.spa_decode_confidence(model, many, N, tt, cc)
+            assert torch.equal(lg.argmax(-1).to(torch.int32).view(B, N), tt)
+            ws.check()
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_changing_the_cache_drops_a_captured_graph():
+    B, N, vocab = 1, 64, 512
+    lp = LayerPair(spa, SHAPE, seed=95, dtype=BF16, max_B=B, max_N=N, std=0.05)
+    e = torch.randn((vocab, SHAPE.d), device="cuda").to(torch.bfloat16)
+    ones = torch.ones((SHAPE.d,), device="cuda").to(torch.bfloat16)
+    h0 = torch.zeros((B, N, SHAPE.d), dtype=torch.bfloat16, device="cuda")
+    model = spa.Model([lp.layer], [lp.cache(B, N)], h0, e, ones, e, vocab, B, N, 0.25, 1, 0.25, 0.25)
+    toks = torch.zeros((B, N), dtype=torch.int32, device="cuda")
+    pos, tok = torch.tensor([[3]], dtype=torch.int32, device="cuda"), torch.empty((1, 1), dtype=torch.int32, device="cuda")
+    model.embed_tokens(toks)
+    spa.spa_decode_step(model, pos, None, 1, 1, tok)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    spa.spa_decode_graph_capture(model, pos, None, 1, tok, stream=s)
+    assert spa.spa_decode_graph_kernel_nodes(model) > 0
+    q8 = spa.Q8Cache(B, N, 2, 128)
+    spa.spa_model_set_q8(model, [q8])
+    assert spa.spa_decode_graph_kernel_nodes(model) == 0
+    with pytest.raises(spa.SpaError) as err:
+        spa.spa_decode_graph_launch(model, stream=s)
+    assert err.value.status == -1
+    wrong = spa.Q8Cache(B, N + 1, 2, 128)
+    with pytest.raises(spa.SpaError) as err:
+        spa.spa_model_set_q8(model, [wrong])
+    assert err.value.status == -2
+    spa.spa_decode_step(model, pos, None, 1, 1, tok)   # still on the cache that was accepted
+    lp.ws.check()
+    assert torch.count_nonzero(q8.k_scale) > 0
+    spa.spa_model_set_q8(model, None)
+    spa.spa_decode_step(model, pos, None, 1, 1, tok)
+    lp.ws.check()

@@ -1,0 +1,109 @@
+"""CPU tests of the argument checks of the 8-bit cache and log-probability
+entry points: every refusal comes before the library touches the device.  A
+workspace needs a GPU, so the checks behind it are driven on the GPU below."""
+import ctypes
+
+import pytest
+import torch
+
+spa = pytest.importorskip("adaptive_hidden_state_b200.spa",
+                          reason="libspa.so not built (python -m adaptive_hidden_state_b200.build)")
+
+
+def test_null_handles_are_refused():
+    c = spa.Q8CacheDesc(16, 16, 16, 16, 1, 8, 1, 128, 64, 0)
+    lc = spa.LayerCacheDesc(16, 16, 16, 16, 1, 8)
+    L = spa.lib
+    assert L.spa_q8_write(None, ctypes.byref(c), 16, 16, 0, None, 1, None) == -1
+    assert L.spa_q8_read(None, ctypes.byref(c), None, 1, 16, 16, None) == -1
+    assert L.spa_q8_attention(None, 16, ctypes.byref(c), None, 16, 1, None) == -1
+    assert L.spa_layer_step_q8(None, 16, ctypes.byref(lc), ctypes.byref(c), 1, 16, None) == -1
+    assert L.spa_full_block_q8(None, 16, ctypes.byref(lc), ctypes.byref(c), 1, None) == -1
+    assert L.spa_model_set_q8(None, ctypes.byref(c)) == -1
+    assert L.spa_token_logprobs(None, 16, 0, 1, 8, 8, 16, 0, 16, 16, None, None, None) == -1
+    assert L.spa_decode_logits(None, 16, 1, 16, None) == -1
+    assert "null" in L.spa_last_error().decode()
+
+
+def test_python_side_refusals():
+    with pytest.raises(ValueError):
+        spa.Q8Cache(1, 8, 1, 128, block=48, device="cpu")
+    with pytest.raises(ValueError):
+        spa.Q8Cache(1, 8, 1, 128, fmt=2, device="cpu")
+    c = spa.Q8Cache(2, 70, 3, 64, block=32, fmt=spa.SPA_Q8_E4M3, device="cpu")
+    assert c.k.shape == (2, 70, 192) and c.k.dtype == torch.float8_e4m3fn and c.k_scale.shape == (2, 3, 3)
+    assert c.desc.block == 32 and c.desc.format == 1 and c.desc.n_kv_heads == 3
+
+    class Ws:
+        desc = spa.LayerDesc(d=256, n_heads=4, head_dim=64, ffn=128, r=1, dtype=spa.SPA_BF16, rms_eps=1e-5,
+                             rope_theta=1e4)
+        handle = None
+
+    x = torch.zeros((2, 1, 192), dtype=torch.bfloat16)
+    for call in (lambda: spa.spa_q8_write(Ws, c, x, x), lambda: spa.spa_q8_read(Ws, c, x, x),
+                 lambda: spa.spa_q8_attention(Ws, torch.zeros((2, 1, 256)), c, torch.zeros((2, 1, 256))),
+                 lambda: spa.spa_token_logprobs(Ws, torch.zeros((2, 8)), None, None, None),
+                 lambda: spa.spa_token_logprobs(Ws, torch.zeros((2, 8, 2)), None, None, None),
+                 lambda: spa.spa_token_logprobs(Ws, torch.zeros((2, 8)).half(), None, None, None),
+                 lambda: spa.spa_token_logprobs(Ws, torch.zeros((8, 2)).T, None, None, None),
+                 lambda: spa.spa_token_logprobs(Ws, torch.zeros((0, 8)), None, None, None)):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.gpu
+def test_refusals_behind_a_workspace():
+    desc = spa.LayerDesc(d=256, n_heads=2, head_dim=128, ffn=128, r=1, dtype=spa.SPA_BF16, rms_eps=1e-5,
+                         rope_theta=1e4)
+    ws = spa.Workspace(desc, 1, 64)
+    before = spa.spa_launch_count()
+    c = spa.Q8Cache(1, 40, 2, 128)
+    L, H = spa.lib, ws.handle
+    q = torch.zeros((1, 4, 256), dtype=torch.bfloat16, device="cuda")
+    P = q.data_ptr()
+
+    def variant(**kw):
+        d = spa.Q8CacheDesc.from_buffer_copy(c.desc)
+        for k, v in kw.items():
+            setattr(d, k, v)
+        return d
+
+    for kw, status in [(dict(k_codes=None), -1), (dict(v_scale=None), -1), (dict(k_codes=c.k.data_ptr() + 4), -1),
+                       (dict(k_scale=c.k_scale.data_ptr() + 1), -1), (dict(format=2), -1), (dict(B=0), -2),
+                       (dict(N=0), -2), (dict(n_kv_heads=0), -2), (dict(B=70000), -2), (dict(N=(1 << 30) + 1), -2),
+                       (dict(head_dim=64), -2), (dict(n_kv_heads=3), -2), (dict(block=48), -5), (dict(block=256), -5)]:
+        d = variant(**kw)
+        assert L.spa_q8_write(H, ctypes.byref(d), P, P, 0, None, 4, None) == status, kw
+        assert L.spa_q8_read(H, ctypes.byref(d), None, 4, P, P, None) == status, kw
+        assert L.spa_q8_attention(H, P, ctypes.byref(d), None, P, 4, None) == status, kw
+    D = ctypes.byref(c.desc)
+    assert L.spa_q8_write(H, None, P, P, 0, None, 4, None) == -1
+    assert L.spa_q8_write(H, D, None, P, 0, None, 4, None) == -1
+    assert L.spa_q8_write(H, D, P + 2, P, 0, None, 4, None) == -1
+    assert L.spa_q8_write(H, D, P, P, 2, None, 4, None) == -1
+    assert L.spa_q8_write(H, D, P, P, 0, None, 0, None) == -2
+    assert L.spa_q8_write(H, D, P, P, 0, None, 41, None) == -2
+    assert L.spa_q8_read(H, D, None, 41, P, P, None) == -2
+    assert L.spa_q8_read(H, D, None, 4, P, None, None) == -1
+    assert L.spa_q8_read(H, D, None, 4, P + 8, P, None) == -1
+    assert L.spa_q8_attention(H, None, D, None, P, 4, None) == -1
+    assert L.spa_q8_attention(H, P, D, None, P + 2, 4, None) == -1
+    assert L.spa_q8_attention(H, P, D, None, P, 0, None) == -2
+    small = spa.LayerDesc(d=256, n_heads=16, head_dim=16, ffn=128, r=1, dtype=spa.SPA_BF16, rms_eps=1e-5,
+                          rope_theta=1e4)
+    ws16 = spa.Workspace(small, 1, 16)
+    assert L.spa_q8_attention(ws16.handle, P, ctypes.byref(variant(head_dim=16)), None, P, 1, None) == -5
+    for args, status in [((None, 0, 1, 8, 8, P, 0, P, P, None, None), -1), ((P, 5, 1, 8, 8, P, 0, P, P, None, None), -1),
+                         ((P + 1, 1, 1, 8, 8, P, 0, P, P, None, None), -1), ((P, 0, 0, 8, 8, P, 0, P, P, None, None), -2),
+                         ((P, 0, 1, 0, 8, P, 0, P, P, None, None), -2), ((P, 0, 2, 8, 7, P, 0, P, P, None, None), -2),
+                         ((P, 0, 1, 8, 8, P, 33, P, P, P, P), -2), ((P, 0, 1, 8, 8, P, -1, P, P, P, P), -2),
+                         ((P, 0, 1, 8, 8, P, 2, P, P, None, P), -1), ((P, 0, 1, 8, 8, None, 0, P, P, None, None), -1)]:
+        assert L.spa_token_logprobs(H, *args, None) == status, args
+    with pytest.raises(ValueError):
+        spa.spa_q8_attention(ws, q.float(), c, q)
+    with pytest.raises(ValueError):
+        spa.spa_q8_attention(ws, q.transpose(1, 2), c, q)
+    with pytest.raises(ValueError):
+        spa.spa_q8_read(ws, c, q, q[:, :2])
+    assert spa.spa_launch_count() == before
+    assert ws.status() == 0
