@@ -1,16 +1,20 @@
 // Log probabilities of given tokens with the entropy and the most likely
 // alternatives of each row of logits, in one pass over the logits.
 //
-// Per row, with m = max x: S = sum e^(x-m), T = sum e^(x-m) (x-m), both kept
-// in fp32 by every thread against its own running maximum and re-scaled when
-// that grows; log p(i) = (x_i - m) - log S and H = log S - T / S, a sum of two
-// terms that are never negative, so a sharp row loses nothing by cancellation.
+// Per row, with m = max x and y = (x - m) log2 e: S = sum 2^y and T = sum 2^y y,
+// both kept in fp32 by every thread against its own running maximum and
+// re-scaled when that grows; log p(i) = (x_i - m) - log S and
+// H = log S - ln 2 T / S, two terms that are never negative, so a sharp row
+// loses nothing by cancellation.  (x - m before the product with log2 e: x
+// log2 e alone leaves the type's range for masks of its lowest value.)
 //
-// The `top` largest: each warp keeps its best 32 in order, one per lane.  An
-// element enters only if it beats the warp's `top`-th best; a thread first
-// compares the maximum of its whole tile, and the warps share the best such
-// bound, so nearly every tile is passed by one comparison.  The order (larger
-// value, then lower id) is total, so the result depends on no timing.
+// The `top` largest: the running maxima of 64 groups of threads give a bound
+// that at least `top` logits reach, raised whenever the number of tiles read
+// has doubled; a thread compares the maximum of its 16 elements with it, and
+// the few elements that reach it (about 1.2 top in each doubling) go to their
+// warp's buffer in shared memory.  A buffer that fills keeps its best `top`.
+// The order (larger value, then lower id) is total, and an entry's place is
+// the number of better ones, so the result depends on no timing.
 //
 // Bound by HBM: 4 or 2 bytes per logit.  A row is read by a cluster of 1 to 8
 // CTAs, whose statistics and lists meet in distributed shared memory: no
@@ -20,24 +24,36 @@
 namespace spa {
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
-constexpr int kLpUnroll = 4;  // 16-byte loads in flight per thread
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kLpBuf = 64;  // candidates a warp holds before it keeps its best
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct LpStat {
-  float m, s, t;
+  float m;     // the largest x seen (-inf: none)
+  float s, t;  // sum 2^y and sum 2^y y with y = (x - m) log2 e
 };
-// Sum of two partial statistics against the larger maximum.  A part without
+// Two partial statistics against the larger maximum.  A part without
 // elements (m = -inf, s = 0) adds nothing; NaN sums stay NaN.
 __device__ __forceinline__ LpStat lp_merge(const LpStat& a, const LpStat& b) {
   LpStat r;
   r.m = fmaxf(a.m, b.m);
   const float ref = r.m == -INFINITY ? 0.f : r.m;
-  const float fa = exp2f((a.m - ref) * kLog2e), fb = exp2f((b.m - ref) * kLog2e);
-  // e^(m_a - m) is 0 long before the difference reaches the clamp
-  const float da = fmaxf(a.m - ref, -1e4f), db = fmaxf(b.m - ref, -1e4f);
+  // 2^d is 0 long before d reaches the bound, which keeps 0 * -inf out of t
+  const float da = fmaxf((a.m - ref) * kLog2e, -1e4f), db = fmaxf((b.m - ref) * kLog2e, -1e4f);
+  const float fa = exp2f(da), fb = exp2f(db);
   r.s = fa * a.s + fb * b.s;
   r.t = fa * (a.t + a.s * da) + fb * (b.t + b.s * db);
   return r;
+}
+// The statistics of lanes 0 .. 2^k - 1 (width = 2^k), in every one of them.
+__device__ __forceinline__ LpStat lp_merge_lanes(LpStat st, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) {
+    LpStat b;
+    b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+    b.t = __shfl_xor_sync(0xffffffffu, st.t, o);
+    st = lp_merge(st, b);
+  }
+  return st;
 }
 
 // Order-preserving map of floats to signed integers (for atomicMax).
@@ -49,31 +65,127 @@ __device__ __forceinline__ float lp_unkey(int k) { return __int_as_float(k ^ ((k
 
 __device__ __forceinline__ bool lp_better(float v, int i, float w, int j) { return v > w || (v == w && i < j); }
 
-// A warp's ordered list (lane i holds the i-th best) and its `top`-th entry.
+// 2^y, 0 below the normal range.
+__device__ __forceinline__ float lp_ex2(float y) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return r;
+}
+// The larger of a and b, NaN if either is NaN.
+__device__ __forceinline__ float lp_max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float lp_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ float2 lp_fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 lp_add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 lp_mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+struct LpEntry {
+  float v;
+  int id;
+};
+
+// A warp's candidates in shared memory.  tv, ti: the top-th best of them
+// after the last compaction.
 struct LpList {
-  float v = -INFINITY, tv = -INFINITY;
-  int i = 0x7FFFFFFF, ti = 0x7FFFFFFF;
-  __device__ __forceinline__ void insert(float cv, int ci, int top, int lane) {
-    const int pos = __popc(__ballot_sync(0xffffffffu, lp_better(v, i, cv, ci)));
-    const float uv = __shfl_up_sync(0xffffffffu, v, 1);
-    const int ui = __shfl_up_sync(0xffffffffu, i, 1);
-    if (lane > pos) { v = uv; i = ui; }
-    if (lane == pos) { v = cv; i = ci; }
-    tv = __shfl_sync(0xffffffffu, v, top - 1);
-    ti = __shfl_sync(0xffffffffu, i, top - 1);
-  }
-  // Every lane's candidate (where `is` holds), in lane order.
-  __device__ __forceinline__ void offer(bool is, float cv, int ci, int top, int lane) {
-    uint32_t mask = __ballot_sync(0xffffffffu, is && lp_better(cv, ci, tv, ti));
-    while (mask) {
-      const int src = __ffs(mask) - 1;
-      mask &= mask - 1;
-      const float sv = __shfl_sync(0xffffffffu, cv, src);
-      const int si = __shfl_sync(0xffffffffu, ci, src);
-      if (lp_better(sv, si, tv, ti)) insert(sv, si, top, lane);
+  LpEntry* e;
+  int n = 0;
+  float tv = -INFINITY;
+  int ti = 0x7FFFFFFF;
+  // Keeps the best `top`, in order: an entry's place is the number of better ones.
+  __device__ __forceinline__ void compact(int top, int lane) {
+    __syncwarp();
+    LpEntry mine[2];
+    int rank[2] = {0, 0};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) mine[q] = lane + 32 * q < n ? e[lane + 32 * q] : LpEntry{-INFINITY, 0x7FFFFFFF};
+    for (int k = 0; k < n; ++k) {
+      const LpEntry o = e[k];
+      rank[0] += lp_better(o.v, o.id, mine[0].v, mine[0].id);
+      rank[1] += lp_better(o.v, o.id, mine[1].v, mine[1].id);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (lane + 32 * q < n && rank[q] < top) e[rank[q]] = mine[q];
+    __syncwarp();
+    if (n >= top) {
+      n = top;
+      tv = e[top - 1].v;
+      ti = e[top - 1].id;
     }
   }
+  // One candidate per lane where `is` holds.
+  __device__ __forceinline__ void offer(bool is, float cv, int ci, int top, int lane, int* s_cut) {
+    uint32_t mask = __ballot_sync(0xffffffffu, is);
+    if (!mask) return;
+    if (n + __popc(mask) > kLpBuf) {
+      compact(top, lane);
+      if (lane == 0 && tv > -INFINITY) atomicMax(s_cut, lp_key(tv));
+      is = is && lp_better(cv, ci, tv, ti);
+      mask = __ballot_sync(0xffffffffu, is);
+    }
+    if (is) e[n + __popc(mask & ((1u << lane) - 1u))] = {cv, ci};
+    n += __popc(mask);
+  }
 };
+
+// Raises the CTA's bound to the top-th largest of the running maxima of 64
+// groups of four threads: at least `top` logits reach it.  Every thread of
+// the CTA; a warp ranks 8 groups, four lanes to one.
+__device__ __forceinline__ void lp_bound(float m, float* s_grp, int* s_cut, int top, int warp, int lane) {
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const int me = warp * 8 + (lane >> 2);
+  if ((lane & 3) == 0) s_grp[me] = m;
+  __syncthreads();
+  int rank = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int q = (k * 4 + (lane & 3)) * 4;
+    const float4 o = *reinterpret_cast<const float4*>(s_grp + q);
+    rank += o.x > m || (o.x == m && q < me);
+    rank += o.y > m || (o.y == m && q + 1 < me);
+    rank += o.z > m || (o.z == m && q + 2 < me);
+    rank += o.w > m || (o.w == m && q + 3 < me);
+  }
+  rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+  rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+  if ((lane & 3) == 0 && rank == top - 1) atomicMax(s_cut, lp_key(m));
+  __syncthreads();
+}
 
 template <typename T> struct LpVec;
 template <> struct LpVec<float> {
@@ -95,64 +207,101 @@ template <> struct LpVec<__nv_bfloat16> {
   }
 };
 
-// NE elements per thread (absent ones -inf): id(i) is element i's column,
-// ascending in i.
-template <int NE, typename IdFn>
-__device__ __forceinline__ void lp_tile(const float (&x)[NE], IdFn id, LpStat& st, LpList& list, int* s_cut,
-                                        int top, int lane) {
+// NE elements per thread (absent ones -inf): VN of consecutive columns from
+// id0, the next VN one CTA's width further.  bound: raise the bound first,
+// with the whole CTA.
+template <int NE, int VN>
+__device__ __forceinline__ void lp_tile(const float (&x)[NE], int id0, LpStat& st, LpList& list,
+                                        int* s_cut, float* s_grp, int top, bool bound, int warp, int lane) {
   float tm = x[0];
 #pragma unroll
-  for (int i = 1; i < NE; ++i) tm = fmaxf(tm, x[i]);
+  for (int i = 1; i + 1 < NE; i += 2) tm = lp_max3(tm, x[i], x[i + 1]);
+  if (NE % 2 == 0) tm = fmaxf(tm, x[NE - 1]);
+  if (bound) lp_bound(fmaxf(tm, st.m), s_grp, s_cut, top, warp, lane);
   if (tm > st.m) {
     const LpStat none = {tm, 0.f, 0.f};
     st = lp_merge(st, none);
   }
   const float ref = st.m == -INFINITY ? 0.f : st.m;
-  float s = 0.f, t = 0.f;
+  // 2^-150 is 0 here; the bound keeps 0 * -inf out of t, and lets NaN pass
+  if constexpr (NE == 1) {
+    const float y = lp_max_nan((x[0] - ref) * kLog2e, -150.f), e = lp_ex2(y);
+    st.s += e;
+    st.t = fmaf(e, y, st.t);
+  } else {
+    float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const float d = x[i] - ref, e = exp2f(d * kLog2e);
-    s += e;
-    t = fmaf(e, fmaxf(d, -1e4f), t);
-  }
-  st.s += s;
-  st.t += t;
-  if (top == 0) return;
-  float cut = lp_unkey(*reinterpret_cast<volatile int*>(s_cut));
-  const bool maybe = tm >= cut && tm > -INFINITY && lp_better(tm, id(0), list.tv, list.ti);
-  if (!__any_sync(0xffffffffu, maybe)) return;
-  if (list.tv == -INFINITY) {
-    // a bound for a list that is not full yet: the top-th largest of the lanes' maxima
-    int rank = 0;
-#pragma unroll
-    for (int q = 0; q < 32; ++q) {
-      const float o = __shfl_sync(0xffffffffu, tm, q);
-      rank += o > tm || (o == tm && q < lane);
+    for (int i = 0; i < NE; i += 2) {
+      float2 y = lp_mul2(lp_add2(make_float2(x[i], x[i + 1]), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
+      y.x = lp_max_nan(y.x, -150.f);
+      y.y = lp_max_nan(y.y, -150.f);
+      const float2 e = make_float2(lp_ex2(y.x), lp_ex2(y.y));
+      s = lp_add2(s, e);
+      t = lp_fma2(e, y, t);
     }
-    const uint32_t at = __ballot_sync(0xffffffffu, rank == top - 1);
-    if (at) cut = fmaxf(cut, __shfl_sync(0xffffffffu, tm, __ffs(at) - 1));
+    st.s += s.x + s.y;
+    st.t += t.x + t.y;
   }
+  if (top == 0) return;
+  const float cut = lp_unkey(*reinterpret_cast<volatile int*>(s_cut));
+  if (!__any_sync(0xffffffffu, tm >= cut && tm > -INFINITY && lp_better(tm, id0, list.tv, list.ti))) return;
+  // the elements that reach the bound, one a lane a turn; few lanes have any
+  uint32_t has = 0;
 #pragma unroll
-  for (int i = 0; i < NE; ++i) list.offer(x[i] >= cut && x[i] > -INFINITY, x[i], id(i), top, lane);
-  if (lane == 0 && list.tv > cut) atomicMax(s_cut, lp_key(list.tv));
+  for (int i = 0; i < NE; ++i) has |= (uint32_t)(x[i] >= cut && x[i] > -INFINITY) << i;
+  while (__any_sync(0xffffffffu, has != 0)) {
+    const int i = has ? __ffs(has) - 1 : 0;
+    const bool is = has != 0;
+    has &= has - 1;
+    const int id = id0 + (i / VN) * kLpThreads * VN + i % VN;
+    float v = x[0];
+#pragma unroll
+    for (int k = 1; k < NE; ++k) v = i == k ? x[k] : v;
+    list.offer(is && lp_better(v, id, list.tv, list.ti), v, id, top, lane, s_cut);
+  }
+}
+
+// Vectors i, i + one CTA's width, ... below v1.
+template <int U>
+__device__ __forceinline__ void lp_fetch(uint4 (&w)[U], const uint4* xv, int i, int v1) {
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (i + u * kLpThreads < v1) w[u] = __ldg(xv + i + u * kLpThreads);
+}
+template <typename T, int U>
+__device__ __forceinline__ void lp_unpack(const uint4 (&w)[U], float* v, int i, int v1) {
+  constexpr int VN = LpVec<T>::N;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (i + u * kLpThreads < v1) {
+      LpVec<T>::unpack(w[u], v + u * VN);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VN; ++e) v[u * VN + e] = -INFINITY;
+    }
+  }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) logp_kernel(const LogpParams p, int C) {
-  constexpr int VN = LpVec<T>::N;
+__global__ void __launch_bounds__(kLpThreads, 4) logp_kernel(const LogpParams p, int C) {
+  constexpr int VN = LpVec<T>::N, U = 16 / VN;  // 16 elements a thread a tile
   __shared__ float s_stat[kLpWarps][3];
-  __shared__ float s_lv[kLpWarps][32];
-  __shared__ int s_li[kLpWarps][32];
+  __shared__ LpEntry s_e[kLpWarps][kLpBuf];     // the warps' candidates
+  __shared__ LpEntry s_c[kLpWarps * kLpBuf];    // those that reach the last bound; later the cluster's lists
+  __shared__ __align__(16) float s_grp[64];
   __shared__ float s_out[3];  // this CTA's statistics and list, read by the cluster's first CTA
-  __shared__ float s_ov[32];
-  __shared__ int s_oi[32];
-  __shared__ int s_cut;
+  __shared__ LpEntry s_o[32];
+  __shared__ int s_cut, s_n;
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)(blockIdx.x % C);
   const long long row = blockIdx.x / C;
-  if (tid == 0) s_cut = lp_key(-INFINITY);
+  if (tid == 0) {
+    s_cut = lp_key(-INFINITY);
+    s_n = 0;
+  }
+  if (tid < 32) s_o[tid] = {-INFINITY, 0x7FFFFFFF};
   __syncthreads();
   const T* x = reinterpret_cast<const T*>(p.logits) + row * p.ld;
   const int top = p.top;
@@ -165,76 +314,114 @@ __global__ void __launch_bounds__(kLpThreads) logp_kernel(const LogpParams p, in
 
   LpStat st = {-INFINITY, 0.f, 0.f};
   LpList list;
-  if (rank == 0 && head) {
-    const float v[1] = {tid < head ? to_f(x[tid]) : -INFINITY};
-    if (warp == 0) lp_tile<1>(v, [&](int) { return tid; }, st, list, &s_cut, top, lane);
+  list.e = s_e[warp];
+  // the next tile's loads are in flight while this one is worked on
+  uint4 cur[U], nxt[U];
+  constexpr int kStep = kLpThreads * U;
+  lp_fetch<U>(nxt, xv, v0 + tid, v1);
+  int tiles = 0;  // read so far; the bound is raised whenever their number doubles
+  // (one copy of the tile's code: straight-line code that runs once or twice waits for its instructions)
+#pragma unroll 1
+  for (int b0 = v0; b0 < v1 || tiles == 0; b0 += kStep, ++tiles) {
+    float v[U * VN];
+#pragma unroll
+    for (int u = 0; u < U; ++u) cur[u] = nxt[u];
+    lp_fetch<U>(nxt, xv, b0 + kStep + tid, v1);
+    lp_unpack<T, U>(cur, v, b0 + tid, v1);
+    lp_tile<U * VN, VN>(v, head + (b0 + tid) * VN, st, list, &s_cut, s_grp, top,
+                        top > 0 && (tiles & (tiles - 1)) == 0, warp, lane);
   }
-  for (int b0 = v0; b0 < v1; b0 += kLpThreads * kLpUnroll) {
-    uint4 w[kLpUnroll];
-    float v[kLpUnroll * VN];
-#pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) {
-      const int i = b0 + u * kLpThreads + tid;
-      if (i < v1) w[u] = __ldg(xv + i);
-    }
-#pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) {
-      if (b0 + u * kLpThreads + tid < v1) {
-        LpVec<T>::unpack(w[u], v + u * VN);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VN; ++e) v[u * VN + e] = -INFINITY;
-      }
-    }
-    const int first = head + (b0 + tid) * VN;
-    lp_tile<kLpUnroll * VN>(v, [&](int i) { return first + (i / VN) * kLpThreads * VN + i % VN; }, st, list,
-                            &s_cut, top, lane);
-  }
-  if (rank == C - 1 && tail0 < p.V) {
-    const float v[1] = {tail0 + tid < p.V ? to_f(x[tail0 + tid]) : -INFINITY};
-    if (warp == 0) lp_tile<1>(v, [&](int) { return tail0 + tid; }, st, list, &s_cut, top, lane);
+  if (warp == 0 && ((rank == 0 && head) || (rank == C - 1 && tail0 < p.V))) {
+    // at most 7 elements on each side: lanes 0-15 before the vectors, 16-31 after them
+    const int id = lane < 16 ? lane : tail0 + lane - 16;
+    const bool in = lane < 16 ? rank == 0 && lane < head : rank == C - 1 && id < p.V;
+    const float v[1] = {in ? to_f(x[id]) : -INFINITY};
+    lp_tile<1, 1>(v, id, st, list, &s_cut, s_grp, top, false, warp, lane);
   }
 
-  // lanes, warps, CTAs of the cluster, each in a fixed order
+  // the CTA's list: an entry's place is the number of better ones among
+  // those that reach the last bound
+  if (top) {
+    lp_bound(st.m, s_grp, &s_cut, top, warp, lane);
+    const float cut = lp_unkey(s_cut);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    LpStat b;
-    b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    b.t = __shfl_xor_sync(0xffffffffu, st.t, o);
-    st = lp_merge(st, b);
+    for (int q = 0; q < kLpBuf / 32; ++q) {
+      const bool is = lane + 32 * q < list.n && list.e[lane + 32 * q].v >= cut;
+      const uint32_t mask = __ballot_sync(0xffffffffu, is);
+      int at = 0;
+      if (mask && lane == 0) at = atomicAdd(&s_n, __popc(mask));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1u));
+      if (is) s_c[at] = list.e[lane + 32 * q];
+    }
   }
+  // lanes, warps, CTAs of the cluster, each in a fixed order
+  st = lp_merge_lanes(st, 32);
   if (lane == 0) {
     s_stat[warp][0] = st.m; s_stat[warp][1] = st.s; s_stat[warp][2] = st.t;
   }
-  s_lv[warp][lane] = list.v;
-  s_li[warp][lane] = list.i;
   __syncthreads();
   if (warp == 0) {
-    for (int w = 1; w < kLpWarps; ++w) {
-      const LpStat b = {s_stat[w][0], s_stat[w][1], s_stat[w][2]};
-      st = lp_merge(st, b);
-      if (top) list.offer(lane < top && s_lv[w][lane] > -INFINITY, s_lv[w][lane], s_li[w][lane], top, lane);
-    }
+    const int w = lane % kLpWarps;
+    st = lp_merge_lanes({s_stat[w][0], s_stat[w][1], s_stat[w][2]}, kLpWarps);
     if (lane == 0) { s_out[0] = st.m; s_out[1] = st.s; s_out[2] = st.t; }
-    s_ov[lane] = list.v;
-    s_oi[lane] = list.i;
   }
+  if (top) {
+    const int n = s_n;
+    for (int k = tid; k < n; k += kLpThreads) {
+      const LpEntry mine = s_c[k];
+      int better = 0;
+#pragma unroll 4
+      for (int q = 0; q < n; ++q) {
+        const LpEntry o = s_c[q];
+        better += lp_better(o.v, o.id, mine.v, mine.id);
+      }
+      if (better < top) s_o[better] = mine;
+    }
+  }
+  const LpEntry* fin = s_o;  // the row's list
   if (C > 1) {
     cluster_sync();
-    if (rank == 0 && warp == 0) {
-      for (int q = 1; q < C; ++q) {
+    if (rank == 0) {
+      // thread (c, place): CTA c's entry
+      const int c = tid >> 5;
+      LpEntry mine = {-INFINITY, 0x7FFFFFFF};
+      if (c < C && lane < top) {
+        const uint32_t at = mapa_shared(smem_u32(&s_o[lane]), c);
+        mine.v = ld_dsmem_f32(at);
+        mine.id = __float_as_int(ld_dsmem_f32(at + 4));
+      }
+      s_c[tid] = mine;
+      if (warp == 0) {
+        const int q = lane % C;  // C is a power of two
         LpStat b;
         b.m = ld_dsmem_f32(mapa_shared(smem_u32(&s_out[0]), q));
         b.s = ld_dsmem_f32(mapa_shared(smem_u32(&s_out[1]), q));
         b.t = ld_dsmem_f32(mapa_shared(smem_u32(&s_out[2]), q));
-        const float cv = ld_dsmem_f32(mapa_shared(smem_u32(&s_ov[lane]), q));
-        const int ci = __float_as_int(ld_dsmem_f32(mapa_shared(smem_u32(&s_oi[lane]), q)));
-        st = lp_merge(st, b);
-        if (top) list.offer(lane < top && cv > -INFINITY, cv, ci, top, lane);
+        st = lp_merge_lanes(b, C);
       }
+      LpEntry* out = s_e[0];  // the warps' candidates are done with
+      if (tid < 32) out[tid] = {-INFINITY, 0x7FFFFFFF};
+      __syncthreads();
+      if (mine.v > -INFINITY) {
+        int better = lane;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (q >= C || q == c) continue;
+          int lo = 0;  // entries of list q (in order, absent ones last) that are better: 0 .. 32
+#pragma unroll
+          for (int step = 16; step > 0; step >>= 1) {
+            const LpEntry o = s_c[q * 32 + lo + step - 1];
+            if (lp_better(o.v, o.id, mine.v, mine.id)) lo += step;
+          }
+          const LpEntry o = s_c[q * 32 + lo];
+          better += lo + lp_better(o.v, o.id, mine.v, mine.id);
+        }
+        if (better < top) out[better] = mine;
+      }
+      fin = out;
     }
   }
+  __syncthreads();
   if (rank == 0 && warp == 0) {
     const bool none = st.m == -INFINITY && st.s == 0.f;  // every logit is -inf
     const float logS = logf(st.s);
@@ -244,20 +431,25 @@ __global__ void __launch_bounds__(kLpThreads) logp_kernel(const LogpParams p, in
       if (tok < 0 || tok >= p.V) report_error(p.err, DEVERR_INDEX, 721);
       else lp = none ? -INFINITY : (to_f(x[tok]) - st.m) - logS;
       p.logp[row] = lp;
-      p.entropy[row] = none ? 0.f : logS - st.t / st.s;
+      p.entropy[row] = none ? 0.f : logS - kLn2 * (st.t / st.s);
     }
     if (lane < top) {
-      const bool has = list.v > -INFINITY;
-      p.top_id[row * top + lane] = has ? list.i : -1;
-      p.top_logp[row * top + lane] = has ? (list.v - st.m) - logS : -INFINITY;
+      const float v = fin[lane].v;
+      const bool has = v > -INFINITY;
+      p.top_id[row * top + lane] = has ? fin[lane].id : -1;
+      p.top_logp[row * top + lane] = has ? (v - st.m) - logS : -INFINITY;
     }
   }
   if (C > 1) cluster_sync();  // the other CTAs' shared memory stays until it has been read
 }
 
 cudaError_t launch_token_logprobs(int dtype, const LogpParams& p, int rows, int num_sms, cudaStream_t stream) {
+  // CTAs per row: as many as the SMs hold at once (four each), each with at
+  // least a tile.  2 rows of 126464: 1 -> 8 CTAs 20.7 -> 9.7 us; 130 rows of
+  // 32003: 1 -> 4 14.9 -> 12.2 us, but 8 (two waves) 19.2 us; 768 rows of
+  // 126464: 1 -> 2 76.8 -> 82.7 us.
   int C = 1;
-  while (C < 8 && (long long)rows * C < 4LL * num_sms && p.V / (2 * C) >= 4096) C *= 2;
+  while (C < 8 && (long long)rows * 2 * C <= 4LL * num_sms && p.V / (2 * C) >= 4096) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows * C);
   cfg.blockDim = dim3(kLpThreads);
