@@ -308,6 +308,8 @@ cudaError_t launch_q8_read(int dtype, int fmt, const Q8ReadParams& p, cudaStream
 // part: scratch for the key shares, sync: [sync_len] ints, zero between launches.
 cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, float* part, size_t part_floats,
                                 size_t sync_len, int num_sms, cudaStream_t stream);
+// The tensor-core kernel for many query rows (bf16, hd 64 or 128).
+cudaError_t launch_q8_attention_tc(int fmt, int hd, Q8AttnParams p, int num_sms, cudaStream_t stream);
 // Per row of logits [rows, V] (row stride ld elements): log probability of
 // tok, entropy, and the `top` largest (ties to the lowest id).
 struct LogpParams {

@@ -65,53 +65,6 @@ __device__ __forceinline__ float lp_unkey(int k) { return __int_as_float(k ^ ((k
 
 __device__ __forceinline__ bool lp_better(float v, int i, float w, int j) { return v > w || (v == w && i < j); }
 
-// 2^y, 0 below the normal range.
-__device__ __forceinline__ float lp_ex2(float y) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
-  return r;
-}
-// The larger of a and b, NaN if either is NaN.
-__device__ __forceinline__ float lp_max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float lp_max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-// Pairs of fp32 in one instruction.
-__device__ __forceinline__ float2 lp_fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b, c;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-__device__ __forceinline__ float2 lp_add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-
-__device__ __forceinline__ float2 lp_mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-
 struct LpEntry {
   float v;
   int id;
@@ -215,7 +168,7 @@ __device__ __forceinline__ void lp_tile(const float (&x)[NE], int id0, LpStat& s
                                         int* s_cut, float* s_grp, int top, bool bound, int warp, int lane) {
   float tm = x[0];
 #pragma unroll
-  for (int i = 1; i + 1 < NE; i += 2) tm = lp_max3(tm, x[i], x[i + 1]);
+  for (int i = 1; i + 1 < NE; i += 2) tm = max3(tm, x[i], x[i + 1]);
   if (NE % 2 == 0) tm = fmaxf(tm, x[NE - 1]);
   if (bound) lp_bound(fmaxf(tm, st.m), s_grp, s_cut, top, warp, lane);
   if (tm > st.m) {
@@ -225,19 +178,19 @@ __device__ __forceinline__ void lp_tile(const float (&x)[NE], int id0, LpStat& s
   const float ref = st.m == -INFINITY ? 0.f : st.m;
   // 2^-150 is 0 here; the bound keeps 0 * -inf out of t, and lets NaN pass
   if constexpr (NE == 1) {
-    const float y = lp_max_nan((x[0] - ref) * kLog2e, -150.f), e = lp_ex2(y);
+    const float y = max_nan((x[0] - ref) * kLog2e, -150.f), e = ex2(y);
     st.s += e;
     st.t = fmaf(e, y, st.t);
   } else {
     float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NE; i += 2) {
-      float2 y = lp_mul2(lp_add2(make_float2(x[i], x[i + 1]), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
-      y.x = lp_max_nan(y.x, -150.f);
-      y.y = lp_max_nan(y.y, -150.f);
-      const float2 e = make_float2(lp_ex2(y.x), lp_ex2(y.y));
-      s = lp_add2(s, e);
-      t = lp_fma2(e, y, t);
+      float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
+      y.x = max_nan(y.x, -150.f);
+      y.y = max_nan(y.y, -150.f);
+      const float2 e = make_float2(ex2(y.x), ex2(y.y));
+      s = add2(s, e);
+      t = fma2(e, y, t);
     }
     st.s += s.x + s.y;
     st.t += t.x + t.y;

@@ -10,7 +10,8 @@
 // probabilities before they are rounded to bf16 (a power of two there moves
 // no rounding).
 //
-// q8_attn_rows_kernel (below) takes 16 query rows per CTA.
+// q8_attn_rows_kernel (below) takes 16 query rows per CTA: single tokens, fp32
+// queries, head_dim 32.  More rows in bf16 go to spa_q8_attn_tc.cu.
 #include <cstring>
 
 #include "spa_q8.cuh"
@@ -399,6 +400,11 @@ static int rows_splits(const Q8AttnParams& p, int hd, int num_sms, size_t part_r
 
 cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, float* part, size_t part_floats,
                                 size_t sync_len, int num_sms, cudaStream_t stream) {
+  // More than one row tile: each key would be converted again for every 16
+  // query rows, which the tensor-core kernel does once for 128 or 256.  At
+  // N = 512, 32 heads of 128: 16 rows 15.7 (this kernel) against 15.5 us, 32
+  // rows 17.5 / 13.4, 128 rows 25.0 / 13.9 us; one row 8.5 / 13.2 us.
+  if (dtype == 1 && hd >= 64 && p.k * p.group > 16) return launch_q8_attention_tc(fmt, hd, p, num_sms, stream);
   p.tiles = (p.k * p.group + 15) / 16;
   const size_t part_rows = part_floats / (hd + 2) / 16 * 16;
   p.splits = rows_splits(p, hd, num_sms, part_rows, sync_len);
