@@ -123,6 +123,31 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// mbar_wait for kernels whose loops should stay in the instruction cache: the
+// waiting loop is one function, and its limit (about a second) is kept in SM
+// clocks.
+constexpr long long kWaitLimitClocks = 2000000000ll;
+static __device__ __noinline__ bool mbar_wait_loop(uint32_t a, uint32_t parity, volatile int* abort, int* err,
+                                                   int site) {
+  const long long t0 = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(a, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitClocks) {
+      *abort = 1;
+      report_error(err, DEVERR_TIMEOUT, site);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait_clk(uint64_t* bar, uint32_t parity, volatile int* abort, int* err,
+                                              int site) {
+  const uint32_t a = smem_u32(bar);
+  return mbar_try_wait(a, parity) || mbar_wait_loop(a, parity, abort, err, site);
+}
+
 // Plain arrive (count one) on an mbarrier of this CTA.
 __device__ __forceinline__ void mbar_arrive_cta(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");

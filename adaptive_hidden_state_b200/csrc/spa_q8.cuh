@@ -44,8 +44,9 @@ template <int FMT> __device__ __forceinline__ uint32_t q8_encode2(float a, float
   }
 }
 
-// Pair of bf16 from the two codes at byte positions 0 and 2 of t (the other
-// bytes are ignored): exact, since a code has at most 8 significant bits.
+// Pair of bf16 from the two codes at byte positions 0 and 2 of t (bytes 1 and
+// 3: anything for int8, the codes' sign bits for e4m3, as q8_pair makes them):
+// exact, since a code has at most 8 significant bits.
 //   int8:  0x4300 | (c & 0x7F) is 128 + (c & 0x7F) and 0x4300 | (c & 0x80) is
 //          128 or 256; their difference is the signed value.
 //   e4m3:  the 7 low bits at bf16's exponent and mantissa positions read as
@@ -56,16 +57,24 @@ template <int FMT> __device__ __forceinline__ uint32_t q8_to_bf162_lo(uint32_t t
     const uint32_t lo = (t & 0x007F007Fu) | 0x43004300u, hi = (t & 0x00800080u) | 0x43004300u;
     r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&hi));
   } else {
-    const uint32_t w = ((t & 0x007F007Fu) << 4) | ((t & 0x00800080u) << 8);
+    const uint32_t w = (t << 4) & 0x87F087F0u;  // t's codes are sign-extended to 16 bits
     const uint32_t f = 0x7B807B80u;  // 2^120
     r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&f));
   }
   return *reinterpret_cast<uint32_t*>(&r);
 }
+// Codes i of x and of y (i = 0..3; 4..7: of the other word) at byte positions 0 and 2.
+template <int FMT> __device__ __forceinline__ uint32_t q8_pair(uint32_t x, uint32_t y, int i, int j) {
+  // a selector with bit 3 set replicates the byte's sign
+  const uint32_t a = (uint32_t)i, b = (uint32_t)j;
+  uint32_t r;  // prmt itself: __byte_perm leaves that bit out
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(a | ((a | 8u) << 4) | (b << 8) | ((b | 8u) << 12)));
+  return r;
+}
 // Four codes of a word -> two bf16 pairs (bytes 0, 1 and bytes 2, 3).
 template <int FMT> __device__ __forceinline__ void q8_word_to_bf16(uint32_t w, uint32_t& p01, uint32_t& p23) {
-  p01 = q8_to_bf162_lo<FMT>(__byte_perm(w, 0, 0x4140));
-  p23 = q8_to_bf162_lo<FMT>(__byte_perm(w, 0, 0x4342));
+  p01 = q8_to_bf162_lo<FMT>(q8_pair<FMT>(w, w, 0, 1));
+  p23 = q8_to_bf162_lo<FMT>(q8_pair<FMT>(w, w, 2, 3));
 }
 
 // One code as float.

@@ -283,10 +283,8 @@ __global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnPar
     }
 #pragma unroll
     for (int j = 0; j < VB; ++j) {
-      // bytes j of the two rows at byte positions 0 and 2
-      const uint32_t sel = 0x0400u + (j & 3) * 0x0101u;
-      const uint32_t b0 = q8_to_bf162_lo<FMT>(__byte_perm(vw[0][j >> 2], vw[1][j >> 2], sel));
-      const uint32_t b1 = q8_to_bf162_lo<FMT>(__byte_perm(vw[2][j >> 2], vw[3][j >> 2], sel));
+      const uint32_t b0 = q8_to_bf162_lo<FMT>(q8_pair<FMT>(vw[0][j >> 2], vw[1][j >> 2], j & 3, 4 + (j & 3)));
+      const uint32_t b1 = q8_to_bf162_lo<FMT>(q8_pair<FMT>(vw[2][j >> 2], vw[3][j >> 2], j & 3, 4 + (j & 3)));
 #pragma unroll
       for (int n = 0; n < NT; ++n) mma_bf16(o[j], pa[n], b0, b1);
     }

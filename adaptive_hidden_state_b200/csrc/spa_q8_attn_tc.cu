@@ -8,10 +8,8 @@
 //   next 4 warps    conversion: codes go from global memory through registers
 //                   (the next tile's loads are in flight while this one is
 //                   converted) to bf16 tiles in shared memory, in the swizzled
-//                   layout the MMA reads; the block's scale, a power of two, is
-//                   multiplied in there, exactly, so the softmax sees plain
-//                   keys and values and both query tiles share the work
-//   last warp       one thread issues the MMAs: for each key tile and query
+//                   layout the MMA reads, once for both query tiles
+//   one warp more   one thread issues the MMAs: for each key tile and query
 //                   tile S = Q K^T (fp32, TMEM), and once the softmax warps
 //                   have written P (bf16) over S in TMEM, O += P V with P as
 //                   the TMEM operand, so P never touches shared memory
@@ -20,6 +18,11 @@
 // order, so QK_i(j) overwrites P_i(j-1) after PV_i(j-1) has read it, and the
 // commit after QK_i(j) that hands S_i to the softmax also says that O_i is
 // complete up to j - 1 and may be re-scaled.
+//
+// The scales stay out of the conversion: a key block's multiplies its scores
+// in the product the softmax makes anyway, a value block's becomes a summand
+// log2 vs in the exponent (so P V needs no other), and the row sum takes each
+// group's sum of p vs times 1 / vs.
 //
 // The running maximum is lazy: O is re-scaled only when it grows by more than
 // 2^8 (the result is exact for any reference).  Key shares of a query tile
@@ -45,7 +48,7 @@ template <int HD, int NQ> struct TcCfg {
 };
 
 struct TcSync {
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done;
+  uint64_t q_full, kv_full[4], kv_empty[4], s_full[2], p_full[2], o_done;  // K stages 0, 1, V stages 2, 3
   uint32_t tmem;
   int abort, ok;
 };
@@ -76,20 +79,59 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void proxy_fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// 16 codes -> 16 bf16 values times the scale (a power of two or 0: exact).
-template <int FMT>
-__device__ __forceinline__ void convert16(const uint4& w4, float scale, uint4& lo, uint4& hi) {
-  const __nv_bfloat162 sc = __float2bfloat162_rn(scale);
-  const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-  uint32_t o[8];
+// True in one lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// mbar_wait for a whole warp: every lane waits, all agree.
+__device__ __forceinline__ bool mma_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int site) {
+  const bool ok = mbar_wait_clk(bar, parity, abort, err, site);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// 16 codes -> 16 bf16 values (without their scale).
+template <int FMT> __device__ __forceinline__ void convert16(const uint4& w4, uint4& lo, uint4& hi) {
+  q8_word_to_bf16<FMT>(w4.x, lo.x, lo.y);
+  q8_word_to_bf16<FMT>(w4.y, lo.z, lo.w);
+  q8_word_to_bf16<FMT>(w4.z, hi.x, hi.y);
+  q8_word_to_bf16<FMT>(w4.w, hi.z, hi.w);
+}
+
+// 32 lanes x 32 columns, not waited for.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Waits for the loads started; reg_tie then keeps the uses of their registers behind the wait.
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void reg_tie(uint32_t* r) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+// Scores of 64 columns of this thread's row; those of keys that do not count
+// (left of them do) -inf.
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&x)[64], int left) {
+  tmem_ld32_start(taddr, x);
+  tmem_ld32_start(taddr + 32u, x + 32);
+  tmem_wait_ld();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t t = q8_to_bf162_lo<FMT>(__byte_perm(w[i >> 1], 0, i & 1 ? 0x4342 : 0x4140));
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&t), sc);
-    o[i] = *reinterpret_cast<const uint32_t*>(&r);
+  for (int c0 = 0; c0 < 64; c0 += 16) reg_tie(x + c0);
+  if (left < 64) {
+    asm volatile("");  // a branch, not 64 selects in every tile
+#pragma unroll
+    for (int q = 0; q < 64; ++q) x[q] = q < left ? x[q] : 0xFF800000u;
   }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 template <int HD, int FMT, int NQ>
@@ -113,11 +155,11 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
 
   if (tid == 0) {
     mbar_init(&sy.q_full, NQ * 128);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sy.kv_full[s], 128);
+      mbar_init(&sy.kv_empty[s], 1);
+    }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sy.k_full[s], 128);
-      mbar_init(&sy.k_empty[s], 1);
-      mbar_init(&sy.v_full[s], 128);
-      mbar_init(&sy.v_empty[s], 1);
       mbar_init(&sy.s_full[s], 1);
       mbar_init(&sy.p_full[s], 128);
     }
@@ -151,50 +193,76 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
   if (warp < kConvWarp) {
     // ------------------------------------------------------------ softmax
     const int i = warp >> 2, row = (warp & 3) * 32 + lane;
-    // Q rows of this tile, 2 (HD = 128) or 4 per instruction of a warp
+    // this thread's query row: its offset in Q and O (-1: past the last row)
+    const int qr = row0 + i * kTT + row;
+    const long long my_off =
+        qr < R ? (((long long)b * p.k + qr / p.group) * p.n_heads + (long long)h * p.group + qr % p.group) * HD : -1;
+    constexpr int CPR = HD / 8;     // 16-byte pieces of a row
+    constexpr int RPI = 32 / CPR;   // rows a warp moves per instruction, each whole
+    uint8_t* qtile = sQ + i * Cfg::kQBytes;
+    auto piece = [&](int it) {      // where this lane's piece of step `it` stands in the swizzled tile
+      const int r = (warp & 3) * 32 + it * RPI + lane / CPR, c = lane % CPR;
+      return qtile + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    };
     {
-      constexpr int CPR = HD / 8;  // 16-byte pieces of a row
-      uint8_t* dst = sQ + i * Cfg::kQBytes;
-#pragma unroll 8
+      uint4 v[CPR];
+#pragma unroll
       for (int it = 0; it < CPR; ++it) {
-        const int r = (warp & 3) * 32 + it * (32 / CPR) + lane / CPR, c = lane % CPR;
-        const int qr = row0 + i * kTT + r;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (qr < R) {
-          const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.Q) +
-                                     (((size_t)b * p.k + qr / p.group) * p.n_heads + (size_t)h * p.group + qr % p.group) * HD;
-          v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-        }
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+        const long long o = __shfl_sync(0xffffffffu, my_off, it * RPI + lane / CPR);
+        v[it] = make_uint4(0u, 0u, 0u, 0u);
+        if (o >= 0) v[it] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.Q) + o) + lane % CPR);
       }
+#pragma unroll
+      for (int it = 0; it < CPR; ++it) *reinterpret_cast<uint4*>(piece(it)) = v[it];
       proxy_fence_smem();
       mbar_arrive_cta(&sy.q_full);
     }
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_base = lane_base + (uint32_t)(i * 128), o_base = lane_base + 256u + (uint32_t)(i * 128);
-    const float c = p.scale_log2;
+    // scales of the tile's 16-key groups: lane g holds the key scale of group
+    // g, lane 8 + g the value scale (1 past the length), a tile ahead
+    const int nb = (p.N + (1 << p.block_log2) - 1) >> p.block_log2;
+    const float* scp = (lane & 8 ? p.v_scale : p.k_scale) + (size_t)b * nb * p.n_kv + h;
+    auto scale_of = [&](int j) {
+      const int key = (kt0 + j) * kTT + (lane & 7) * 16;
+      return j < n && key < len ? __ldg(scp + (size_t)(key >> p.block_log2) * p.n_kv) : 1.f;
+    };
+    float sc_next = scale_of(0);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      const bool got = mbar_wait(&sy.s_full[i], j & 1, &sy.abort, err, 732);
+      // key scale: times log2 e / sqrt(hd); value scale: 2^(y + log2 vs) is p vs,
+      // and the sum of a group's p is its sum over vs.  A scale of 0 (its
+      // codes are converted to zeros) counts as 1.
+      const float sc = sc_next == 0.f ? 1.f : sc_next;
+      const float pre = lane & 8 ? log2f(sc) : sc * p.scale_log2;
+      const float rcp = 1.0f / sc;
+      sc_next = scale_of(j + 1);
+      const bool got = mbar_wait_clk(&sy.s_full[i], j & 1, &sy.abort, err, 732);
       __syncwarp();
       if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
       tc_fence_after();
       const int left = len - (kt0 + j) * kTT;  // keys of this tile that count
+      // Two passes over the scores in TMEM, 64 columns at a time: the loops
+      // of all warps together have to stay in the instruction caches (with
+      // a row's 128 scores in registers and one long pass, every role waited
+      // for instructions: 4600 cycles a tile pair against 3600).
       float tmax = -INFINITY;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kTT; c0 += 32) {
-        float x[32];
-        tmem_ld32(s_base + (uint32_t)c0, x);
-        if (left < c0 + 32) {
+      for (int c0 = 0; c0 < kTT; c0 += 64) {
+        uint32_t x[64];
+        load_scores(s_base + (uint32_t)c0, x, left - c0);
 #pragma unroll
-          for (int q = 0; q < 32; ++q) x[q] = c0 + q < left ? x[q] : -INFINITY;
+        for (int g = 0; g < 4; ++g) {
+          const float* xg = reinterpret_cast<const float*>(x + 16 * g);
+          float gm = max3(xg[0], xg[1], xg[2]);
+#pragma unroll
+          for (int q = 3; q < 15; q += 2) gm = max3(gm, xg[q], xg[q + 1]);
+          gm = fmaxf(gm, xg[15]);
+          tmax = fmaxf(tmax, gm * __shfl_sync(0xffffffffu, pre, (c0 >> 4) + g));
         }
-#pragma unroll
-        for (int q = 0; q < 32; q += 2) tmax = max3(tmax, x[q], x[q + 1]);
       }
-      tmax *= c;
       if (j == 0) {
         m = tmax;
       } else if (__any_sync(0xffffffffu, tmax > m + kTRescale)) {
@@ -209,7 +277,8 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
               : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
                 "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
               : "r"(o_base + (uint32_t)c0));
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          tmem_wait_ld();
+          reg_tie(o);
 #pragma unroll
           for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
           tmem_st16(o_base + (uint32_t)c0, o);
@@ -217,32 +286,37 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
         l *= f;
         m = m_new;
       }
-      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
-      for (int c0 = 0; c0 < kTT; c0 += 32) {
-        float x[32];
-        uint32_t w[16];
-        tmem_ld32(s_base + (uint32_t)c0, x);
-        if (left < c0 + 32) {
+      for (int c0 = 0; c0 < kTT; c0 += 64) {
+        uint32_t x[64], w[32];
+        load_scores(s_base + (uint32_t)c0, x, left - c0);
 #pragma unroll
-          for (int q = 0; q < 32; ++q) x[q] = c0 + q < left ? x[q] : -INFINITY;
-        }
+        for (int g = 0; g < 4; ++g) {
+          const int sg = (c0 >> 4) + g;
+          const float a = __shfl_sync(0xffffffffu, pre, sg), bb = __shfl_sync(0xffffffffu, pre, 8 + sg) - m;
+          const float rv = __shfl_sync(0xffffffffu, rcp, 8 + sg);
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int q = 0; q < 32; q += 2) {
-          const float2 y = fma2(make_float2(x[q], x[q + 1]), make_float2(c, c), make_float2(-m, -m));
-          const float2 e = make_float2(ex2(y.x), ex2(y.y));
-          sum = add2(sum, e);
-          const __nv_bfloat162 v = __floats2bfloat162_rn(e.x, e.y);
-          w[q >> 1] = *reinterpret_cast<const uint32_t*>(&v);
+          for (int q = 0; q < 16; q += 2) {
+            const int k = 16 * g + q;
+            const float2 y = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), make_float2(a, a),
+                                  make_float2(bb, bb));
+            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            sum = add2(sum, e);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(e.x, e.y);
+            w[k >> 1] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          l = fmaf(sum.x + sum.y, rv, l);
         }
-        tmem_st16(s_base + (uint32_t)(c0 >> 1), w);  // over scores this thread has read
+        // over scores this thread has read: columns c0 / 2 .. c0 / 2 + 31 <= c0 + 63
+        tmem_st16(s_base + (uint32_t)(c0 >> 1), *reinterpret_cast<const uint32_t(*)[16]>(w));
+        tmem_st16(s_base + (uint32_t)(c0 >> 1) + 16u, *reinterpret_cast<const uint32_t(*)[16]>(w + 16));
       }
-      l += sum.x + sum.y;
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive_cta(&sy.p_full[i]);
     }
-    const bool fin = ok && mbar_wait(&sy.o_done, 0, &sy.abort, err, 733);
+    const bool fin = ok && mbar_wait_clk(&sy.o_done, 0, &sy.abort, err, 733);
     __syncwarp();
     const bool warp_ok = __all_sync(0xffffffffu, fin);
     if (lane == 0 && !warp_ok) atomicAnd(&sy.ok, 0);
@@ -250,12 +324,7 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
     named_bar_sync(1, NQ * 128);
     if (sy.ok) {
       tc_fence_after();
-      const int qr = row0 + i * kTT + row;
       const float inv = l != 0.f ? 1.0f / l : 0.f;
-      __nv_bfloat16* dst = nullptr;
-      if (S == 1 && qr < R)
-        dst = reinterpret_cast<__nv_bfloat16*>(p.O) +
-              (((size_t)b * p.k + qr / p.group) * p.n_heads + (size_t)h * p.group + qr % p.group) * HD;
       // key shares: the unnormalised row into the idle rings, 16-byte piece c of row r at piece c ^ (r % 16)
       float* sO = reinterpret_cast<float*>(sK) + (size_t)(i * kTT + row) * HD;
 #pragma unroll 1
@@ -268,23 +337,34 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
           for (int q = 0; q < 32; ++q) o[q] = 0.f;
         }
         if (S == 1) {
-          if (dst) {
+          // bf16 rows into the idle Q tile, swizzled as Q was, to be stored as whole rows
 #pragma unroll
-            for (int q = 0; q < 32; q += 8) {
-              uint32_t w[4];
+          for (int q = 0; q < 32; q += 8) {
+            uint32_t w[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(o[q + 2 * e] * inv, o[q + 2 * e + 1] * inv);
-                w[e] = *reinterpret_cast<const uint32_t*>(&v);
-              }
-              *reinterpret_cast<uint4*>(dst + c0 + q) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(o[q + 2 * e] * inv, o[q + 2 * e + 1] * inv);
+              w[e] = *reinterpret_cast<const uint32_t*>(&v);
             }
+            const int c = (c0 + q) >> 3;
+            *reinterpret_cast<uint4*>(qtile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
 #pragma unroll
           for (int q = 0; q < 32; q += 4)
             *reinterpret_cast<float4*>(sO + ((((c0 + q) >> 2) ^ (row & 15)) << 2)) =
                 make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+        }
+      }
+      if (S == 1) {
+        __syncwarp();  // a warp moves its own 32 rows
+#pragma unroll
+        for (int it = 0; it < CPR; ++it) {
+          const long long o = __shfl_sync(0xffffffffu, my_off, it * RPI + lane / CPR);
+          if (o >= 0)
+            *(reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.O) + o) + lane % CPR) =
+                *reinterpret_cast<const uint4*>(piece(it));
         }
       }
       if (S > 1) {
@@ -303,89 +383,106 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
     const int nb = (p.N + (1 << p.block_log2) - 1) >> p.block_log2;
     const float* ksc = p.k_scale + (size_t)b * nb * p.n_kv + h;
     const float* vsc = p.v_scale + (size_t)b * nb * p.n_kv + h;
-    const int tr = t / CPR, tc = t % CPR;
-    uint4 kr[PER], vr[PER];
-    float kf[PER], vf[PER];
-    auto fetch = [&](const uint8_t* base, const float* scale, int j, uint4 (&r)[PER], float (&f)[PER]) {
+    // Eight neighbouring threads take four pieces of two rows: their 16-byte
+    // stores, two pieces apart in a row and swizzled by the row, hit every bank once.
+    const int tr = HD == 128 ? (t >> 4) * 2 + ((t >> 2) & 1) : t / CPR;
+    const int tc = HD == 128 ? (t & 3) + ((t >> 3) & 1) * 4 : t % CPR;
+    // the swizzle depends on row % 8, which the steps of ROWS rows leave alone
+    const int off = (tc >> 2) * 16384 + tr * 128, x7 = tr & 7;
+    const int off0 = off + ((((tc & 3) * 2) ^ x7) << 4), off1 = off + ((((tc & 3) * 2 + 1) ^ x7) << 4);
+    // half u: K (u even) or V (u odd) of tile u / 2; its codes are loaded while half u - 1 is converted
+    uint4 r[PER];
+    auto fetch = [&](int u) {
+      const uint8_t* base = (u & 1 ? vbase : kbase) + tc * 16;
+      const int key0 = (kt0 + (u >> 1)) * kTT + tr;
 #pragma unroll
       for (int it = 0; it < PER; ++it) {
-        const int key = (kt0 + j) * kTT + it * ROWS + tr;
+        const int key = key0 + it * ROWS;
         r[it] = make_uint4(0u, 0u, 0u, 0u);
-        f[it] = 0.f;
-        if (j < n && key < len) {  // rows past the length are zeros, whatever the cache holds there
-          r[it] = __ldg(reinterpret_cast<const uint4*>(base + (size_t)key * width) + tc);
-          f[it] = __ldg(scale + (size_t)(key >> p.block_log2) * p.n_kv);
-        }
+        if (key < len)  // rows past the length are zeros, whatever the cache holds there
+          r[it] = __ldg(reinterpret_cast<const uint4*>(base + (size_t)key * width));
       }
     };
-    auto put = [&](uint8_t* tile, const uint4 (&r)[PER], const float (&f)[PER]) {
+    // bits g and 8 + g: 16-key group g of tile j has a key or a value scale of 0
+    auto zero_groups = [&](int j) {
+      const int key = (kt0 + j) * kTT + (lane & 7) * 16;
+      const bool z = j < n && key < len && __ldg((lane & 8 ? vsc : ksc) + (size_t)(key >> p.block_log2) * p.n_kv) == 0.f;
+      return __ballot_sync(0xffffffffu, z);
+    };
+    uint32_t zero = 0, zero_next = zero_groups(0);
+    if (n > 0) fetch(0);
+#pragma unroll 1
+    for (int u = 0; u < 2 * n; ++u) {
+      const int j = u >> 1, st = (u & 1) * 2 + (j & 1);
+      if (!(u & 1)) {
+        zero = zero_next;
+        zero_next = zero_groups(j + 1);
+      }
+      if (j >= 2 && !mbar_wait_clk(&sy.kv_empty[st], ((j >> 1) - 1) & 1, &sy.abort, err, 734)) break;
+      uint8_t* tile = sK + st * Cfg::kTile;
+      if (zero & 0xFFu) {
+#pragma unroll
+        for (int it = 0; it < PER; ++it)
+          if ((zero >> ((it * ROWS + tr) >> 4)) & 1) r[it] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      zero >>= 8;
 #pragma unroll
       for (int it = 0; it < PER; ++it) {
-        const int row = it * ROWS + tr;
         uint4 lo, hi;
-        convert16<FMT>(r[it], f[it], lo, hi);
-        uint8_t* dst = tile + (tc >> 2) * 16384 + row * 128;
-        const int c0 = (tc & 3) * 2, x = row & 7;
-        // lanes of the two halves store their pieces in opposite order: every bank once
-        const bool swap = (tc >> 2) & 1;
-        *reinterpret_cast<uint4*>(dst + (((c0 + (swap ? 1 : 0)) ^ x) << 4)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(dst + (((c0 + (swap ? 0 : 1)) ^ x) << 4)) = swap ? lo : hi;
+        convert16<FMT>(r[it], lo, hi);
+        *reinterpret_cast<uint4*>(tile + off0 + it * ROWS * 128) = lo;
+        *reinterpret_cast<uint4*>(tile + off1 + it * ROWS * 128) = hi;
       }
-    };
-    fetch(kbase, ksc, 0, kr, kf);
-    fetch(vbase, vsc, 0, vr, vf);
-#pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      const int st = j & 1;
-      const uint32_t ph = ((j >> 1) - 1) & 1;
-      if (j >= 2 && !mbar_wait(&sy.k_empty[st], ph, &sy.abort, err, 734)) break;
-      put(sK + st * Cfg::kTile, kr, kf);
       proxy_fence_smem();
-      mbar_arrive_cta(&sy.k_full[st]);
-      fetch(kbase, ksc, j + 1, kr, kf);
-      if (j >= 2 && !mbar_wait(&sy.v_empty[st], ph, &sy.abort, err, 735)) break;
-      put(sV + st * Cfg::kTile, vr, vf);
-      proxy_fence_smem();
-      mbar_arrive_cta(&sy.v_full[st]);
-      fetch(vbase, vsc, j + 1, vr, vf);
+      mbar_arrive_cta(&sy.kv_full[st]);
+      if (u + 1 < 2 * n) fetch(u + 1);
     }
-  } else if (lane == 0) {
+  } else {
     // ---------------------------------------------------------------- MMA
+    // The whole warp runs the loop and one elected lane issues, so that
+    // addresses and descriptors stay in uniform registers.
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, HD) | (1u << 16);  // V is MN-major
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dq = smem_desc_sw128(smem_u32(sQ));
     const uint64_t dk = smem_desc_sw128(smem_u32(sK));
     const uint64_t dv = desc_sw128_mn(smem_u32(sV), 16384);
     constexpr uint64_t kTileOff = Cfg::kTile >> 4, kQOff = Cfg::kQBytes >> 4;
-    bool ok = n > 0 && mbar_wait(&sy.q_full, 0, &sy.abort, err, 736);
+    bool ok = n > 0 && mma_wait(&sy.q_full, 0, &sy.abort, err, 736);
+#pragma unroll 1
     for (int j = 0; ok && j <= n; ++j) {
-      const int st = j & 1, pst = (j - 1) & 1;
-      if (j < n && !mbar_wait(&sy.k_full[st], (j >> 1) & 1, &sy.abort, err, 737)) break;
-      if (j > 0 && !mbar_wait(&sy.v_full[pst], ((j - 1) >> 1) & 1, &sy.abort, err, 738)) break;
-#pragma unroll
+      const int st = j & 1, pst = st ^ 1;
+      if (j < n && !mma_wait(&sy.kv_full[st], (j >> 1) & 1, &sy.abort, err, 737)) break;
+      if (j > 0 && !mma_wait(&sy.kv_full[2 + pst], ((j - 1) >> 1) & 1, &sy.abort, err, 738)) break;
+#pragma unroll 1
       for (int i = 0; i < NQ; ++i) {
         if (j > 0) {
-          if (!mbar_wait(&sy.p_full[i], (j - 1) & 1, &sy.abort, err, 739)) { ok = false; break; }
+          if (!mma_wait(&sy.p_full[i], (j - 1) & 1, &sy.abort, err, 739)) { ok = false; break; }
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(tmem + 256u + i * 128u, tmem + i * 128u + kk * 8u, dv + pst * kTileOff + (uint64_t)(kk * 128),
-                         idesc_pv, (j > 1 || kk > 0) ? 1u : 0u);
-          if (i == NQ - 1) umma_commit(&sy.v_empty[pst]);
+            for (int kk = 0; kk < 8; ++kk)
+              umma_bf16_ts(tm + 256u + i * 128u, tm + i * 128u + kk * 8u, dv + pst * kTileOff + (uint64_t)(kk * 128),
+                           idesc_pv, (j > 1 || kk > 0) ? 1u : 0u);
+            if (i == NQ - 1) umma_commit(&sy.kv_empty[2 + pst]);
+          }
         }
         if (j < n) {
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);
-            umma_bf16(tmem + i * 128u, dq + i * kQOff + off, dk + st * kTileOff + off, idesc_qk, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < HD / 16; ++kk) {
+              const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);
+              umma_bf16(tm + i * 128u, dq + i * kQOff + off, dk + st * kTileOff + off, idesc_qk, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&sy.s_full[i]);
+            if (i == NQ - 1) umma_commit(&sy.kv_empty[st]);
           }
-          umma_commit(&sy.s_full[i]);
-          if (i == NQ - 1) umma_commit(&sy.k_empty[st]);
         }
       }
     }
-    umma_commit(&sy.o_done);
+    __syncwarp();
+    if (elect_one()) umma_commit(&sy.o_done);
   }
   __syncwarp();
   __syncthreads();
