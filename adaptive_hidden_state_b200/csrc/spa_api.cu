@@ -1034,11 +1034,11 @@ static int run_q8_write(spa_workspace* ws, const void* k_rows, const void* v_row
   p.k_rows = k_rows; p.v_rows = v_rows; p.idx = idx; p.indexed = indexed;
   p.k_codes = (uint8_t*)c->k_codes; p.v_codes = (uint8_t*)c->v_codes;
   p.k_scale = c->k_scale; p.v_scale = c->v_scale;
-  p.B = c->B; p.N = c->N; p.k = k; p.n_kv = c->n_kv_heads; p.hd = c->head_dim; p.block = c->block;
+  p.B = c->B; p.N = c->N; p.k = k; p.n_kv = c->n_kv_heads; p.hd = c->head_dim;
   p.err = ws->err;
   const double rows = 2.0 * c->B * k * c->n_kv_heads * c->head_dim;
   ProfScope ps(&ws->prof, SPA_PROF_MISC, rows * ((bf ? 2 : 4) + 1), 0.0, s);
-  const cudaError_t e = launch_q8_write(bf, c->format, p, s);
+  const cudaError_t e = launch_q8_write(bf, c->format, c->block, p, ws->num_sms, s);
   if (e != cudaSuccess) return fail(SPA_ERR_CUDA, "8-bit cache write launch: %s", cudaGetErrorString(e));
   return SPA_OK;
 }
@@ -1085,8 +1085,8 @@ extern "C" int spa_q8_read(spa_workspace* ws, const spa_q8_cache* c, const int32
   if (!k_out || !v_out) return fail(SPA_ERR_INVALID, "null output");
   if (!aligned16(k_out) || !aligned16(v_out)) return fail(SPA_ERR_INVALID, "outputs must be 16-byte aligned");
   if (k < 1 || (!idx && k > c->N)) return fail(SPA_ERR_SHAPE, "k=%d outside [1, N=%d]", k, c->N);
+  if (c->B > 32767) return fail(SPA_ERR_SHAPE, "B beyond the launch limit (32767)");
   const long long chunks = (long long)c->n_kv_heads * c->head_dim / 16;
-  if ((long long)c->B * k > ((1LL << 31) - 1) * 256 / chunks) return fail(SPA_ERR_SHAPE, "more rows than a launch takes");
   SPA_TRY(check_device(ws));
   const int bf = ws->desc.dtype == SPA_BF16;
   cudaStream_t s = (cudaStream_t)stream;
@@ -1095,10 +1095,10 @@ extern "C" int spa_q8_read(spa_workspace* ws, const spa_q8_cache* c, const int32
   p.k_codes = (const uint8_t*)c->k_codes; p.v_codes = (const uint8_t*)c->v_codes;
   p.k_scale = c->k_scale; p.v_scale = c->v_scale;
   p.idx = idx; p.k_out = k_out; p.v_out = v_out;
-  p.B = c->B; p.N = c->N; p.k = k; p.n_kv = c->n_kv_heads; p.hd = c->head_dim; p.block = c->block;
+  p.B = c->B; p.N = c->N; p.k = k; p.n_kv = c->n_kv_heads; p.hd = c->head_dim;
   p.err = ws->err;
   ProfScope ps(&ws->prof, SPA_PROF_MISC, 32.0 * c->B * k * chunks * ((bf ? 2 : 4) + 1), 0.0, s);
-  const cudaError_t e = launch_q8_read(bf, c->format, p, s);
+  const cudaError_t e = launch_q8_read(bf, c->format, c->block, p, s);
   if (e != cudaSuccess) return fail(SPA_ERR_CUDA, "8-bit cache read launch: %s", cudaGetErrorString(e));
   return SPA_OK;
 }

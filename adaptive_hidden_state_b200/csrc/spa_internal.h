@@ -279,7 +279,8 @@ struct Q8WriteParams {
   const int32_t* idx;           // [B, k] cache rows (null: 0 .. k - 1)
   uint8_t *k_codes, *v_codes;
   float *k_scale, *v_scale;
-  int B, N, k, n_kv, hd, block, indexed;
+  int B, N, k, n_kv, hd, indexed;
+  int block_log2, hd_log2, by_row, share;  // set by the launch
   int* err;
 };
 struct Q8ReadParams {
@@ -287,7 +288,8 @@ struct Q8ReadParams {
   const float *k_scale, *v_scale;
   const int32_t* idx;           // [B, k] cache rows (null: 0 .. k - 1)
   void *k_out, *v_out;          // [B, k, n_kv * hd]
-  int B, N, k, n_kv, hd, block;
+  int B, N, k, n_kv, hd;
+  int block_log2, hd_log2, wide;    // set by the launch
   int* err;
 };
 struct Q8AttnParams {
@@ -303,8 +305,9 @@ struct Q8AttnParams {
   float scale_log2;             // log2(e) / sqrt(hd)
 };
 // dtype 0 fp32, 1 bf16; fmt 0 int8, 1 e4m3; hd 32, 64 or 128; block 16, 32, 64 or 128.
-cudaError_t launch_q8_write(int dtype, int fmt, const Q8WriteParams& p, cudaStream_t stream);
-cudaError_t launch_q8_read(int dtype, int fmt, const Q8ReadParams& p, cudaStream_t stream);
+cudaError_t launch_q8_write(int dtype, int fmt, int block, Q8WriteParams p, int num_sms,
+                            cudaStream_t stream);
+cudaError_t launch_q8_read(int dtype, int fmt, int block, Q8ReadParams p, cudaStream_t stream);
 // part: scratch for the key shares, sync: [sync_len] ints, zero between launches.
 cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, float* part, size_t part_floats,
                                 size_t sync_len, int num_sms, cudaStream_t stream);

@@ -17,8 +17,6 @@ namespace spa {
 
 constexpr int kQ8Int8 = 0, kQ8E4m3 = 1;
 
-template <int FMT> __device__ __forceinline__ float q8_max() { return FMT == kQ8Int8 ? 127.f : 448.f; }
-
 // Smallest power of two s >= 2^-126 with a <= qmax * s (0 for a = 0; a finite).
 // 127 = 1.984375 * 2^6 and 448 = 1.75 * 2^8: compare mantissas, adjust exponents.
 template <int FMT> __device__ __forceinline__ float q8_scale(float a) {
@@ -34,15 +32,6 @@ template <int FMT> __device__ __forceinline__ float q8_scale(float a) {
 }
 // 1 / s of a scale q8_scale returned (2^-126 .. 2^122): exact.
 __device__ __forceinline__ float q8_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
-
-// Two codes of the pair of values (a, b), already divided by the scale.
-template <int FMT> __device__ __forceinline__ uint32_t q8_encode2(float a, float b) {
-  if constexpr (FMT == kQ8Int8) {
-    return ((uint32_t)__float2int_rn(a) & 0xFFu) | (((uint32_t)__float2int_rn(b) & 0xFFu) << 8);
-  } else {
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  }
-}
 
 // Pair of bf16 from the two codes at byte positions 0 and 2 of t (bytes 1 and
 // 3: anything for int8, the codes' sign bits for e4m3, as q8_pair makes them):
