@@ -136,7 +136,8 @@ template <int FMT> __device__ __forceinline__ uint32_t q8_encode4(const float (&
 //
 // The CTAs count the blocks (by_row = 0; one without a new row is left
 // untouched), or, when there are fewer rows than blocks, the rows: the first
-// row of a block takes it.
+// row of a block takes it (one row in 65536 tokens x 8 heads, blocks of 128:
+// 3.9 against 7.5 us; 64 rows 5.9 / 9.8).
 constexpr int kQwWarps = 4, kQwThreads = kQwWarps * 32;
 constexpr int kQwUnroll = 8;  // 16-byte loads in flight per lane
 

@@ -9,6 +9,7 @@
 // would round every remaining row, and the cache rewrites scattered rows in
 // every step.)  The price is up to one bit of an int8 code's range.
 #pragma once
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "spa_device.cuh"
@@ -64,6 +65,21 @@ template <int FMT> __device__ __forceinline__ uint32_t q8_pair(uint32_t x, uint3
 template <int FMT> __device__ __forceinline__ void q8_word_to_bf16(uint32_t w, uint32_t& p01, uint32_t& p23) {
   p01 = q8_to_bf162_lo<FMT>(q8_pair<FMT>(w, w, 0, 1));
   p23 = q8_to_bf162_lo<FMT>(q8_pair<FMT>(w, w, 2, 3));
+}
+
+// The same to f16 pairs, times 2^-8 for e4m3 (which q8_f16_unit puts right):
+// fewer instructions than to bf16, for operands whose range is under control.
+//   int8:  0x6400 | (c + 128) is 1152 + c; minus 1152.
+//   e4m3:  the 7 low bits at f16's exponent and mantissa positions.
+template <int FMT> __device__ __forceinline__ float q8_f16_unit() { return FMT == kQ8Int8 ? 1.f : 256.f; }
+template <int FMT> __device__ __forceinline__ uint32_t q8_pair_f16(uint32_t x, uint32_t y, int i, int j) {
+  if constexpr (FMT == kQ8Int8) {
+    const uint32_t t = (q8_pair<FMT>(x, y, i, j) & 0x00FF00FFu) ^ 0x64806480u, c = 0x64806480u;
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&t), *reinterpret_cast<const __half2*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    return (q8_pair<FMT>(x, y, i, j) << 7) & 0xBF80BF80u;
+  }
 }
 
 // One code as float.

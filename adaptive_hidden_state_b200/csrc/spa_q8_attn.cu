@@ -4,11 +4,10 @@
 // of a sequence form the R = k * group query rows of that kv head (row
 // r = query r / group, head r % group).
 //
-// The codes are exact in bf16 (at most 8 significant bits), so the products
-// run on the tensor cores in bf16 with fp32 sums, and the scales stay outside
-// them: a key block's scale multiplies its scores, a value block's scale the
-// probabilities before they are rounded to bf16 (a power of two there moves
-// no rounding).
+// The codes are exact in 16-bit floating point (at most 8 significant bits),
+// so the products run on the tensor cores with fp32 sums, and the scales stay
+// outside them: a key block's scale multiplies its scores, a value block's
+// scale the probabilities before they are rounded.
 //
 // q8_attn_rows_kernel (below) takes 16 query rows per CTA: single tokens, fp32
 // queries, head_dim 32.  More rows in bf16 go to spa_q8_attn_tc.cu.
@@ -22,28 +21,37 @@ namespace spa {
 // Row kernel: 16 query rows of one kv head and one contiguous share of its
 // keys per CTA.
 //
-// Each of the four warps walks its own chunks of 16 keys with its own running
+// Each of the four warps walks its own chunks of 32 keys with its own running
 // maximum m, sum l and output, fed by its own ring of asynchronous 16-byte
-// copies (no barrier between warps), so the copies of three chunks are in
+// copies (no barrier between warps), so the copies of two chunks are in
 // flight per warp.  m16n8k16 products: the order of the head elements within
 // a step is free as long as Q and K agree, so a thread reads its HD/4
 // elements of a key as whole 16-byte pieces; likewise the columns of V, of
 // which a thread takes HD/8 consecutive ones.  The ring's 16-byte pieces are
 // permuted within 128-byte lines so that these reads hit every bank once.
 //
-// fp32 queries: Q and P are each the sum of three bf16 terms (24 bits), so
-// three products give the fp32 result to fp32 accuracy.
+// Operands are f16, to which codes go in half of bf16's instructions (those
+// bound the kernel, not HBM, with bf16: 167 against 113 us for one token over
+// 4 x 65536 tokens, 8 kv heads of 128).  Their range is kept by powers of
+// two: a query row is scaled to a largest magnitude of 2^14 .. 2^15 (39 bits
+// lie below it, and bf16's 8 significant bits are exact), a probability times
+// its block's scale over the largest scale so far, at most 1, is held times
+// 2^15 and re-scaled with O when that scale grows.  A probability keeps 11
+// bits where bf16 has 8.
+//
+// fp32 queries: Q and P are each the sum of three f16 terms (24 bits and
+// more), so three products give the fp32 result to fp32 accuracy.
 //
 // The warps' results are joined in shared memory in warp order, and the key
 // shares of a row tile through global scratch by the last CTA to arrive, in
 // share order: the result does not depend on timing.
 // ---------------------------------------------------------------------------
 constexpr int kRWarps = 4, kRThreads = kRWarps * 32;
-constexpr int kRKeys = 16;    // keys of a chunk
-constexpr int kRStages = 4;   // chunks in a warp's ring
+constexpr int kRKeys = 32;    // keys of a chunk
+constexpr int kRStages = 3;   // chunks in a warp's ring
 
 template <int HD> struct RowCfg {
-  static constexpr int kStageBytes = 2 * kRKeys * HD + 16;  // K codes, V codes, the two scales
+  static constexpr int kStageBytes = 2 * kRKeys * HD + 16;  // K codes, V codes, key and value scales of 16 keys
   static constexpr int kRing = kRWarps * kRStages * kStageBytes;
   static constexpr int kJoin = kRWarps * 16 * (HD + 2) * 4;
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
@@ -60,31 +68,27 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Byte offset of 16-byte piece c of row r (16 rows of HD bytes).
+// Byte offset of 16-byte piece c of row r (rows of HD bytes).
 template <int HD> __device__ __forceinline__ int row_piece(int r, int c) {
   constexpr int RPL = 128 / HD, CPR = HD / 16, MUL = HD == 128 ? 1 : 2;
   const int line = r / RPL;
   return line * 128 + ((((r % RPL) * CPR + c) ^ ((MUL * line) & 7)) << 4);
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-// The leading bf16 term of (a, b), which is subtracted from them.
-__device__ __forceinline__ uint32_t split_bf16(float& a, float& b) {
-  const uint32_t w = pack_bf16(a, b);
-  a -= __uint_as_float(w << 16);
-  b -= __uint_as_float(w & 0xFFFF0000u);
-  return w;
+// The leading f16 term of (a, b), which is subtracted from them.
+__device__ __forceinline__ uint32_t split_f16(float& a, float& b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  a -= __low2float(h);
+  b -= __high2float(h);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // NB bytes of shared memory at p into words.
@@ -103,7 +107,7 @@ template <int NB> __device__ __forceinline__ void lds_words(uint32_t (&w)[NB / 4
 template <typename T, int HD, int FMT>
 __global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int NT = sizeof(T) == 4 ? 3 : 1;  // bf16 terms of a query element and of a probability
+  constexpr int NT = sizeof(T) == 4 ? 3 : 1;  // f16 terms of a query element and of a probability
   constexpr int KW = HD / 16;                 // words of a key a thread reads = k16 steps of Q K^T
   constexpr int VB = HD / 8;                  // consecutive columns of V a thread reads = n8 tiles of P V
   constexpr int SB = RowCfg<HD>::kStageBytes;
@@ -124,32 +128,6 @@ __global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnPar
   const int nch = (len + kRKeys - 1) / kRKeys;
   const int c0 = (int)((long long)sp * nch / S), c1 = (int)((long long)(sp + 1) * nch / S);
 
-  // this thread's Q elements: rows g and g + 8, elements tig * HD/4 ..
-  uint32_t q[NT][KW][4];
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = tile * 16 + g + 8 * half;
-    const bool ok = r < R;
-    const int i = ok ? r / p.group : 0, gh = ok ? r % p.group : 0;
-    const T* src = reinterpret_cast<const T*>(p.Q) +
-                   (((size_t)b * p.k + i) * p.n_heads + (size_t)h * p.group + gh) * HD + tig * (HD / 4);
-#pragma unroll
-    for (int s = 0; s < KW; ++s) {
-      if constexpr (NT == 1) {
-        const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(src) + s) : make_uint2(0u, 0u);
-        q[0][s][half] = w.x;
-        q[0][s][2 + half] = w.y;
-      } else {
-        float4 v = ok ? __ldg(reinterpret_cast<const float4*>(src) + s) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          q[n][s][half] = split_bf16(v.x, v.y);
-          q[n][s][2 + half] = split_bf16(v.z, v.w);
-        }
-      }
-    }
-  }
-
   const size_t width = (size_t)p.n_kv * HD;
   const uint8_t* kbase = p.k_codes + (size_t)b * p.N * width + (size_t)h * HD;
   const uint8_t* vbase = p.v_codes + (size_t)b * p.N * width + (size_t)h * HD;
@@ -158,26 +136,70 @@ __global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnPar
   const float* vsc = p.v_scale + (size_t)b * nb * p.n_kv + h;
   uint8_t* ring = smem + warp * kRStages * SB;
 
+  // this lane's pieces of a chunk: piece pc of rows pr, pr + RPI, ...
+  constexpr int CPR = HD / 16, RPI = 32 / CPR, STEPS = kRKeys / RPI;
+  const int pr = lane / CPR, pc = lane % CPR;
   auto fetch = [&](int c, int st) {  // chunk c (always committed, empty past the end)
     if (c < c1) {
       uint8_t* dst = ring + st * SB;
+      const int key0 = c * kRKeys;
+      const size_t off = (size_t)(key0 + pr) * width + pc * 16;
+      const uint8_t *ks = kbase + off, *vs = vbase + off;
+      const size_t step = (size_t)RPI * width;
 #pragma unroll
-      for (int it = 0; it < 2 * kRKeys * (HD / 16) / 32; ++it) {
-        const int e = it * 32 + lane;
-        const int is_v = e / (kRKeys * (HD / 16)), f = e % (kRKeys * (HD / 16));
-        const int r = f / (HD / 16), cc = f % (HD / 16);
-        const int key = c * kRKeys + r;
-        const bool ok = key < len;  // rows past the end arrive as zeros and are not read
-        const uint8_t* src = (is_v ? vbase : kbase) + (size_t)(ok ? key : 0) * width + cc * 16;
-        cp_async16(smem_u32(dst + is_v * kRKeys * HD + row_piece<HD>(r, cc)), src, ok ? 16 : 0);
+      for (int it = 0; it < STEPS; ++it) {
+        const uint32_t d = smem_u32(dst) + row_piece<HD>(pr + it * RPI, pc);
+        // rows past the end arrive as zeros and are not read
+        const bool ok = key0 + pr + it * RPI < len;
+        cp_async16(d, ok ? ks + it * step : kbase, ok ? 16 : 0);
+        cp_async16(d + kRKeys * HD, ok ? vs + it * step : vbase, ok ? 16 : 0);
       }
-      if (lane < 2) {
-        const size_t j = (size_t)((c * kRKeys) >> p.block_log2) * p.n_kv;
-        cp_async4(smem_u32(dst + 2 * kRKeys * HD + 4 * lane), (lane ? vsc : ksc) + j);
+      if (lane < 4) {  // key scales of keys 0-15 and 16-31, value scales
+        const int key = min(key0 + 16 * (lane & 1), len - 1);
+        cp_async4(smem_u32(dst + 2 * kRKeys * HD + 4 * lane),
+                  (lane & 2 ? vsc : ksc) + (size_t)(key >> p.block_log2) * p.n_kv);
       }
     }
     cp_async_commit();
   };
+
+  int cf = c0 + warp;
+#pragma unroll
+  for (int st = 0; st < kRStages - 1; ++st, cf += kRWarps) fetch(cf, st);
+  // this thread's Q elements: rows g and g + 8, elements tig * HD/4 .., scaled
+  // to f16's range; cs: what turns a score back, in units of log2
+  uint32_t q[NT][KW][4];
+  float cs[2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = tile * 16 + g + 8 * half;
+    const bool ok = r < R;
+    const int i = ok ? r / p.group : 0, gh = ok ? r % p.group : 0;
+    const T* src = reinterpret_cast<const T*>(p.Q) +
+                   (((size_t)b * p.k + i) * p.n_heads + (size_t)h * p.group + gh) * HD + tig * (HD / 4);
+    float4 v[KW];
+    float most = 0.f;
+#pragma unroll
+    for (int s = 0; s < KW; ++s) {
+      v[s] = ok ? load4(src + 4 * s) : make_float4(0.f, 0.f, 0.f, 0.f);
+      most = fmaxf(fmaxf(most, fmaxf(fabsf(v[s].x), fabsf(v[s].y))), fmaxf(fabsf(v[s].z), fabsf(v[s].w)));
+    }
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    // 2^(14 - exponent), within 2^-113 .. 2^113 so that it and its inverse are normal
+    const int e = min(max((int)(__float_as_uint(most) >> 23), 127 + 14 - 113), 127 + 14 + 113);
+    const float qs = __uint_as_float((uint32_t)(2 * 127 + 14 - e) << 23);
+    cs[half] = p.scale_log2 * q8_f16_unit<FMT>() * __uint_as_float((uint32_t)(e - 14) << 23);
+#pragma unroll
+    for (int s = 0; s < KW; ++s) {
+      v[s].x *= qs; v[s].y *= qs; v[s].z *= qs; v[s].w *= qs;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        q[n][s][half] = split_f16(v[s].x, v[s].y);
+        q[n][s][2 + half] = split_f16(v[s].z, v[s].w);
+      }
+    }
+  }
 
   float o[VB][4];
 #pragma unroll
@@ -185,25 +207,24 @@ __global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnPar
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float vref = 0.f, vinv = 0.f;  // O is held times vinv = 2^15 / vref, vref the largest value scale so far
 
-  int cf = c0 + warp;
-#pragma unroll
-  for (int st = 0; st < kRStages - 1; ++st, cf += kRWarps) fetch(cf, st);
   int st = 0;
+#pragma unroll 1
   for (int c = c0 + warp; c < c1; c += kRWarps) {
     cp_async_wait<kRStages - 2>();
     __syncwarp();
-    fetch(cf, (st + kRStages - 1) % kRStages);
+    fetch(cf, st == 0 ? kRStages - 1 : st - 1);
     cf += kRWarps;
     const uint8_t* sk = ring + st * SB;
     const uint8_t* sv = sk + kRKeys * HD;
-    const float2 sc = *reinterpret_cast<const float2*>(sk + 2 * kRKeys * HD);
-    st = (st + 1) % kRStages;
+    const float4 sc = *reinterpret_cast<const float4*>(sk + 2 * kRKeys * HD);
+    st = st == kRStages - 1 ? 0 : st + 1;
 
-    // S = Q K^T, two n8 tiles of keys
-    float s[2][4];
+    // S = Q K^T, four n8 tiles of keys
+    float s[4][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < 4; ++t) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
       uint32_t kw[KW];
@@ -220,33 +241,42 @@ __global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnPar
       }
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
-        uint32_t b0, b1;
-        q8_word_to_bf16<FMT>(kw[i], b0, b1);
+        const uint32_t b0 = q8_pair_f16<FMT>(kw[i], kw[i], 0, 1), b1 = q8_pair_f16<FMT>(kw[i], kw[i], 2, 3);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_bf16(s[t], q[n][i], b0, b1);
+        for (int n = 0; n < NT; ++n) mma_f16(s[t], q[n][i], b0, b1);
       }
     }
     // scores in units of log2, keys past the end out
-    const float ks = sc.x * p.scale_log2;
-    const int key0 = c * kRKeys + tig * 2;
-    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[t][e] = key0 + t * 8 + (e & 1) < len ? s[t][e] * ks : -INFINITY;
-        mx[e >> 1] = fmaxf(mx[e >> 1], s[t][e]);
-      }
+    float mx[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      const float a0 = sc.x * cs[i], a1 = sc.y * cs[i];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 2 * i; e < 2 * i + 2; ++e) s[t][e] *= t < 2 ? a0 : a1;
+    }
+    const int left = len - c * kRKeys;
+    if (left < kRKeys) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] = t * 8 + tig * 2 + (e & 1) < left ? s[t][e] : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mx[i] = fmaxf(max3(s[0][2 * i], s[0][2 * i + 1], s[1][2 * i]),
+                    max3(max3(s[1][2 * i + 1], s[2][2 * i], s[2][2 * i + 1]), s[3][2 * i], s[3][2 * i + 1]));
       mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
       mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
       mx[i] = fmaxf(mx[i], m[i]);
     }
-    if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
-      const float f0 = exp2f(m[0] - mx[0]), f1 = exp2f(m[1] - mx[1]);
-      l[0] *= f0;
-      l[1] *= f1;
+    const float vmost = fmaxf(sc.z, sc.w);
+    if (vmost > vref || __any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+      const float grow = fmaxf(vmost, vref), fv = grow > 0.f ? vref / grow : 0.f;
+      const float e0 = ex2(m[0] - mx[0]), e1 = ex2(m[1] - mx[1]), f0 = e0 * fv, f1 = e1 * fv;
+      l[0] *= e0;
+      l[1] *= e1;
 #pragma unroll
       for (int j = 0; j < VB; ++j) {
         o[j][0] *= f0; o[j][1] *= f0;
@@ -254,41 +284,52 @@ __global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnPar
       }
       m[0] = mx[0];
       m[1] = mx[1];
+      vref = grow;
+      vinv = grow > 0.f ? 32768.f / grow : 0.f;
     }
-    uint32_t pa[NT][4];
-    {
-      float pr[2][4];
+    // P, then O += P V for keys 0-15 and 16-31: keys 2 tig, 2 tig + 1 and
+    // those + 8; columns g * VB ..
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const float w = (kk ? sc.w : sc.z) * vinv;
+      uint32_t pa[NT][4];
+      float pv[2][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          pr[t][e] = exp2f(s[t][e] - m[e >> 1]);
-          l[e >> 1] += pr[t][e];
-          pr[t][e] *= sc.y;
+          const float pr_ = ex2(s[2 * kk + t][e] - m[e >> 1]);
+          l[e >> 1] += pr_;
+          pv[t][e] = pr_ * w;
         }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        pa[n][0] = split_bf16(pr[0][0], pr[0][1]);
-        pa[n][1] = split_bf16(pr[0][2], pr[0][3]);
-        pa[n][2] = split_bf16(pr[1][0], pr[1][1]);
-        pa[n][3] = split_bf16(pr[1][2], pr[1][3]);
+        pa[n][0] = split_f16(pv[0][0], pv[0][1]);
+        pa[n][1] = split_f16(pv[0][2], pv[0][3]);
+        pa[n][2] = split_f16(pv[1][0], pv[1][1]);
+        pa[n][3] = split_f16(pv[1][2], pv[1][3]);
+      }
+      uint32_t vw[4][VB / 4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = kk * 16 + tig * 2 + (i & 1) + (i >> 1) * 8;
+        lds_words<VB>(vw[i], sv + row_piece<HD>(r, g * VB / 16) + (g * VB) % 16);
+      }
+#pragma unroll
+      for (int j = 0; j < VB; ++j) {
+        const uint32_t b0 = q8_pair_f16<FMT>(vw[0][j >> 2], vw[1][j >> 2], j & 3, 4 + (j & 3));
+        const uint32_t b1 = q8_pair_f16<FMT>(vw[2][j >> 2], vw[3][j >> 2], j & 3, 4 + (j & 3));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_f16(o[j], pa[n], b0, b1);
       }
     }
-    // O += P V: keys 2 tig, 2 tig + 1 and those + 8; columns g * VB ..
-    uint32_t vw[4][VB / 4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = tig * 2 + (i & 1) + (i >> 1) * 8;
-      lds_words<VB>(vw[i], sv + row_piece<HD>(r, g * VB / 16) + (g * VB) % 16);
-    }
-#pragma unroll
-    for (int j = 0; j < VB; ++j) {
-      const uint32_t b0 = q8_to_bf162_lo<FMT>(q8_pair<FMT>(vw[0][j >> 2], vw[1][j >> 2], j & 3, 4 + (j & 3)));
-      const uint32_t b1 = q8_to_bf162_lo<FMT>(q8_pair<FMT>(vw[2][j >> 2], vw[3][j >> 2], j & 3, 4 + (j & 3)));
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mma_bf16(o[j], pa[n], b0, b1);
-    }
   }
+  // back to units of the values
+  const float unit = vref * (q8_f16_unit<FMT>() / 32768.f);
+#pragma unroll
+  for (int j = 0; j < VB; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[j][e] *= unit;
   cp_async_wait<0>();
   __syncthreads();
 
@@ -381,13 +422,14 @@ static cudaError_t launch_rows(const Q8AttnParams& p, cudaStream_t stream) {
   return launch_k(kern, dim3(p.tiles * p.splits, p.n_kv, p.B), dim3(kRThreads), RowCfg<HD>::kSmem, stream, p);
 }
 
-// Key shares of a row tile: enough CTAs to keep about three on each SM (their
-// copies in flight are what reaches the HBM rate), each with at least two
-// chunks per warp, within the scratch.
+// Key shares of a row tile: as many CTAs as the SMs hold by shared memory (two
+// each for hd 128, four for 64: one token over 4 x 65536 tokens x 8 kv heads
+// of 64 72 against 89 us with two), each with a chunk for every warp, within
+// the scratch.
 static int rows_splits(const Q8AttnParams& p, int hd, int num_sms, size_t part_rows, size_t sync_len) {
   const long long groups = (long long)p.B * p.n_kv * p.tiles;
-  const int most = p.N / (2 * kRKeys * kRWarps);
-  long long s = 3LL * num_sms / groups;
+  const int most = (p.N + kRKeys * kRWarps - 1) / (kRKeys * kRWarps);
+  long long s = (long long)(256 / hd) * num_sms / groups;
   s = s < most ? s : most;
   s = s < 64 ? s : 64;
   if (groups > (long long)sync_len) s = 1;
