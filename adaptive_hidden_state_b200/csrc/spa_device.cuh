@@ -347,6 +347,12 @@ __device__ __forceinline__ float ex2(float y) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
   return r;
 }
+// log2 of a positive normal number (absolute error about 2^-22).
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // The larger of a and b, NaN if either is NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;

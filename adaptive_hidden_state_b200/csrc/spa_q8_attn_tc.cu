@@ -2,22 +2,23 @@
 // queries, head_dim 64 or 128: the kernel for many query rows of a kv head.
 //
 // One CTA = one or two tiles of 128 query rows of one kv head of one
-// sequence, and one contiguous share of its keys, in tiles of 128:
+// sequence, and one contiguous share of its keys, in tiles of 64:
 //   warps 0-3, 4-7  softmax of the first and second query tile: thread i owns
 //                   row i (TMEM lane i)
 //   next 4 warps    conversion: codes go from global memory through registers
 //                   (the next tile's loads are in flight while this one is
 //                   converted) to bf16 tiles in shared memory, in the swizzled
 //                   layout the MMA reads, once for both query tiles
-//   one warp more   one thread issues the MMAs: for each key tile and query
-//                   tile S = Q K^T (fp32, TMEM), and once the softmax warps
-//                   have written P (bf16) over S in TMEM, O += P V with P as
+//   a warp more for each query tile: one thread issues the tile's MMAs: S = Q K^T
+//                   (fp32, TMEM) into one of two buffers of the tile, and, once the
+//                   softmax warps have written P (bf16) over S, O += P V with P as
 //                   the TMEM operand, so P never touches shared memory
-// The order PV0(j-1), QK0(j), PV1(j-1), QK1(j) keeps the tensor core on one
-// query tile while the other's softmax runs.  MMAs of one thread execute in
-// order, so QK_i(j) overwrites P_i(j-1) after PV_i(j-1) has read it, and the
-// commit after QK_i(j) that hands S_i to the softmax also says that O_i is
-// complete up to j - 1 and may be re-scaled.
+// Two score buffers of 64 keys each let the softmax of a query tile go from
+// one key tile to the next without waiting for PV and the next QK^T (one
+// buffer of 128 keys: 225 against XX us for k = 512 of N = 2048, B = 8,
+// 32 heads of 128; a QK^T of 64 keys costs 48 cycles a step where 32 would be
+// half of one of 128).  MMAs of one thread execute in order, so QK_i(j + 2)
+// overwrites P_i(j) after PV_i(j) has read it.
 //
 // The scales stay out of the conversion: a key block's multiplies its scores
 // in the product the softmax makes anyway, a value block's becomes a summand
@@ -34,21 +35,23 @@
 
 namespace spa {
 
-constexpr int kTT = 128;                 // query rows of a tile, keys of a tile
+constexpr int kTT = 128;                 // query rows of a tile
+constexpr int kTK = 64;                  // keys of a tile
 constexpr float kTRescale = 8.0f;
 
 template <int HD, int NQ> struct TcCfg {
   static constexpr int kQBytes = kTT * HD * 2;        // one query tile
-  static constexpr int kTile = kTT * HD * 2;          // one bf16 K or V tile
-  static constexpr int kStages = 2;                   // K ring, V ring
-  static constexpr int kThreads = NQ * 128 + 128 + 32;
+  static constexpr int kTile = kTK * HD * 2;          // one bf16 K or V tile
+  static constexpr int kStages = 4;                   // K ring, V ring
+  static constexpr int kThreads = NQ * 128 + 128 + NQ * 32;
   static constexpr int kUsed = NQ * kQBytes + 2 * kStages * kTile + 1024;
   // at least 120 KB, so that no SM holds two CTAs that want its tensor memory
   static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
 };
 
 struct TcSync {
-  uint64_t q_full, kv_full[4], kv_empty[4], s_full[2], p_full[2], o_done;  // K stages 0, 1, V stages 2, 3
+  uint64_t q_full, kv_full[8], kv_empty[8], o_done;  // K stages 0-3, V stages 4-7
+  uint64_t s_full[4], p_full[4], pv_done[2];         // [2 * query tile + score buffer], [query tile]
   uint32_t tmem;
   int abort, ok;
 };
@@ -79,18 +82,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void proxy_fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// True in one lane of a converged warp (the same one every time).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-// mbar_wait for a whole warp: every lane waits, all agree.
-__device__ __forceinline__ bool mma_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int site) {
-  const bool ok = mbar_wait_clk(bar, parity, abort, err, site);
-  return __all_sync(0xffffffffu, ok);
-}
-
 // 16 codes -> 16 bf16 values (without their scale).
 template <int FMT> __device__ __forceinline__ void convert16(const uint4& w4, uint4& lo, uint4& hi) {
   q8_word_to_bf16<FMT>(w4.x, lo.x, lo.y);
@@ -119,6 +110,25 @@ __device__ __forceinline__ void reg_tie(uint32_t* r) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
+// This thread's O row times f.  Rare, so kept out of the loop's instructions.
+template <int HD> static __device__ __noinline__ void scale_rows(uint32_t o_base, float f) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < HD; c0 += 16) {
+    uint32_t o[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
+          "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+        : "r"(o_base + (uint32_t)c0));
+    tmem_wait_ld();
+    reg_tie(o);
+#pragma unroll
+    for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+    tmem_st16(o_base + (uint32_t)c0, o);
+  }
+}
+
 // Scores of 64 columns of this thread's row; those of keys that do not count
 // (left of them do) -inf.
 __device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&x)[64], int left) {
@@ -143,6 +153,9 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
   uint8_t* sK = sQ + NQ * Cfg::kQBytes;
   uint8_t* sV = sK + Cfg::kStages * Cfg::kTile;
   __shared__ __align__(8) TcSync sy;
+  // per key tile (ring of 8): the four 16-key groups' score factors, log2 of
+  // their value scales and those scales' inverses
+  __shared__ __align__(16) float s_sc[8][12];
   __shared__ float s_m[NQ * kTT], s_l[NQ * kTT];
   __shared__ float s_w[NQ * kTT][8];
 
@@ -155,15 +168,17 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
 
   if (tid == 0) {
     mbar_init(&sy.q_full, NQ * 128);
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < 8; ++s) {
       mbar_init(&sy.kv_full[s], 128);
-      mbar_init(&sy.kv_empty[s], 1);
+      mbar_init(&sy.kv_empty[s], NQ);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&sy.s_full[s], 1);
       mbar_init(&sy.p_full[s], 128);
     }
-    mbar_init(&sy.o_done, 1);
+    mbar_init(&sy.pv_done[0], 1);
+    mbar_init(&sy.pv_done[1], 1);
+    mbar_init(&sy.o_done, NQ);
     sy.abort = 0;
     sy.ok = 1;
     fence_mbar_init();
@@ -176,7 +191,7 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
   __syncthreads();
   tc_fence_after();
   griddep_launch_dependents();  // the next kernel comes to this SM after the tensor memory has been taken
-  const uint32_t tmem = sy.tmem;  // S_i (P_i over it) at columns 128 i, O_i at 256 + 128 i
+  const uint32_t tmem = sy.tmem;  // S_i (P_i over it) at columns 128 i and 128 i + 64, O_i at 256 + 128 i
   griddep_wait();
   int len = p.N;
   if (p.lens) {
@@ -186,7 +201,7 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
       len = min(max(len, 0), p.N);
     }
   }
-  const int n_kt = (len + kTT - 1) / kTT;
+  const int n_kt = (len + kTK - 1) / kTK;
   const int kt0 = (int)((long long)sp * n_kt / S), kt1 = (int)((long long)(sp + 1) * n_kt / S);
   const int n = kt1 - kt0;  // key tiles of this CTA (may be none)
 
@@ -219,102 +234,71 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
     }
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_base = lane_base + (uint32_t)(i * 128), o_base = lane_base + 256u + (uint32_t)(i * 128);
-    // scales of the tile's 16-key groups: lane g holds the key scale of group
-    // g, lane 8 + g the value scale (1 past the length), a tile ahead
-    const int nb = (p.N + (1 << p.block_log2) - 1) >> p.block_log2;
-    const float* scp = (lane & 8 ? p.v_scale : p.k_scale) + (size_t)b * nb * p.n_kv + h;
-    auto scale_of = [&](int j) {
-      const int key = (kt0 + j) * kTT + (lane & 7) * 16;
-      return j < n && key < len ? __ldg(scp + (size_t)(key >> p.block_log2) * p.n_kv) : 1.f;
-    };
-    float sc_next = scale_of(0);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      // key scale: times log2 e / sqrt(hd); value scale: 2^(y + log2 vs) is p vs,
-      // and the sum of a group's p is its sum over vs.  A scale of 0 (its
-      // codes are converted to zeros) counts as 1.
-      const float sc = sc_next == 0.f ? 1.f : sc_next;
-      const float pre = lane & 8 ? log2f(sc) : sc * p.scale_log2;
-      const float rcp = 1.0f / sc;
-      sc_next = scale_of(j + 1);
-      const bool got = mbar_wait_clk(&sy.s_full[i], j & 1, &sy.abort, err, 732);
+      const bool got = mbar_wait_clk(&sy.s_full[2 * i + (j & 1)], (j >> 1) & 1, &sy.abort, err, 732);
       __syncwarp();
       if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
       tc_fence_after();
-      const int left = len - (kt0 + j) * kTT;  // keys of this tile that count
-      // Two passes over the scores in TMEM, 64 columns at a time: the loops
-      // of all warps together have to stay in the instruction caches (with
-      // a row's 128 scores in registers and one long pass, every role waited
-      // for instructions: 4600 cycles a tile pair against 3600).
+      const uint32_t s_at = s_base + (uint32_t)((j & 1) * kTK);
+      uint32_t x[kTK];
+      load_scores(s_at, x, len - (kt0 + j) * kTK);
+      // written by the conversion warps before the tile whose scores these are
+      const float4 a4 = *reinterpret_cast<const float4*>(s_sc[j & 7]), lv4 = *reinterpret_cast<const float4*>(s_sc[j & 7] + 4);
+      const float4 rv4 = *reinterpret_cast<const float4*>(s_sc[j & 7] + 8);
+      const float a[4] = {a4.x, a4.y, a4.z, a4.w}, lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
+      const float rv[4] = {rv4.x, rv4.y, rv4.z, rv4.w};
       float tmax = -INFINITY;
-#pragma unroll 1
-      for (int c0 = 0; c0 < kTT; c0 += 64) {
-        uint32_t x[64];
-        load_scores(s_base + (uint32_t)c0, x, left - c0);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float* xg = reinterpret_cast<const float*>(x + 16 * g);
-          float gm = max3(xg[0], xg[1], xg[2]);
+      for (int g = 0; g < 4; ++g) {
+        const float* xg = reinterpret_cast<const float*>(x + 16 * g);
+        float gm = max3(xg[0], xg[1], xg[2]);
 #pragma unroll
-          for (int q = 3; q < 15; q += 2) gm = max3(gm, xg[q], xg[q + 1]);
-          gm = fmaxf(gm, xg[15]);
-          tmax = fmaxf(tmax, gm * __shfl_sync(0xffffffffu, pre, (c0 >> 4) + g));
-        }
+        for (int q = 3; q < 15; q += 2) gm = max3(gm, xg[q], xg[q + 1]);
+        gm = fmaxf(gm, xg[15]);
+        tmax = fmaxf(tmax, gm * a[g]);
       }
       if (j == 0) {
         m = tmax;
       } else if (__any_sync(0xffffffffu, tmax > m + kTRescale)) {
-        // some row's maximum grew by more than 2^8: the warp re-scales
+        // some row's maximum grew by more than 2^8: the warp re-scales, once
+        // the PV before this one is complete
+        const bool pv = mbar_wait_clk(&sy.pv_done[i], (j - 1) & 1, &sy.abort, err, 741);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, pv)) { ok = false; break; }
+        tc_fence_after();
         const float m_new = fmaxf(m, tmax), f = exp2f(m - m_new);
-#pragma unroll 1
-        for (int c0 = 0; c0 < HD; c0 += 16) {
-          uint32_t o[16];
-          asm volatile(
-              "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-              "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-              : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-                "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-              : "r"(o_base + (uint32_t)c0));
-          tmem_wait_ld();
-          reg_tie(o);
-#pragma unroll
-          for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
-          tmem_st16(o_base + (uint32_t)c0, o);
-        }
+        scale_rows<HD>(o_base, f);
         l *= f;
         m = m_new;
       }
-#pragma unroll 1
-      for (int c0 = 0; c0 < kTT; c0 += 64) {
-        uint32_t x[64], w[32];
-        load_scores(s_base + (uint32_t)c0, x, left - c0);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int sg = (c0 >> 4) + g;
-          const float a = __shfl_sync(0xffffffffu, pre, sg), bb = __shfl_sync(0xffffffffu, pre, 8 + sg) - m;
-          const float rv = __shfl_sync(0xffffffffu, rcp, 8 + sg);
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[16];
+#pragma unroll
+        for (int gg = 0; gg < 2; ++gg) {
+          const int g = 2 * half + gg;
+          const float bb = lv[g] - m;
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int q = 0; q < 16; q += 2) {
             const int k = 16 * g + q;
-            const float2 y = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), make_float2(a, a),
-                                  make_float2(bb, bb));
+            const float2 y = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])),
+                                  make_float2(a[g], a[g]), make_float2(bb, bb));
             const float2 e = make_float2(ex2(y.x), ex2(y.y));
             sum = add2(sum, e);
             const __nv_bfloat162 v = __floats2bfloat162_rn(e.x, e.y);
-            w[k >> 1] = *reinterpret_cast<const uint32_t*>(&v);
+            w[8 * gg + (q >> 1)] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          l = fmaf(sum.x + sum.y, rv, l);
+          l = fmaf(sum.x + sum.y, rv[g], l);
         }
-        // over scores this thread has read: columns c0 / 2 .. c0 / 2 + 31 <= c0 + 63
-        tmem_st16(s_base + (uint32_t)(c0 >> 1), *reinterpret_cast<const uint32_t(*)[16]>(w));
-        tmem_st16(s_base + (uint32_t)(c0 >> 1) + 16u, *reinterpret_cast<const uint32_t(*)[16]>(w + 16));
+        tmem_st16(s_at + (uint32_t)(16 * half), w);  // over the scores, which are in registers
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive_cta(&sy.p_full[i]);
+      mbar_arrive_cta(&sy.p_full[2 * i + (j & 1)]);
     }
     const bool fin = ok && mbar_wait_clk(&sy.o_done, 0, &sy.abort, err, 733);
     __syncwarp();
@@ -375,114 +359,118 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
   } else if (warp < kMmaWarp) {
     // --------------------------------------------------------- conversion
     const int t = tid - kConvWarp * 32;
-    constexpr int CPR = HD / 16, PER = CPR;  // 16-byte pieces of a row; pieces a thread converts (128 rows / 128 threads)
-    constexpr int ROWS = 128 / CPR;          // rows per step of the 128 threads (16 or 32)
+    constexpr int CPR = HD / 16;          // 16-byte pieces of a row
+    constexpr int PER = kTK * CPR / 128;  // pieces of a tile a thread converts (4 or 2)
+    constexpr int ROWS = 128 / CPR;       // rows per step of the 128 threads (16 or 32)
+    constexpr int HALF = kTK * 128;       // bytes of a tile's 64 columns
     const size_t width = (size_t)p.n_kv * HD;
-    const uint8_t* kbase = p.k_codes + (size_t)b * p.N * width + (size_t)h * HD;
-    const uint8_t* vbase = p.v_codes + (size_t)b * p.N * width + (size_t)h * HD;
     const int nb = (p.N + (1 << p.block_log2) - 1) >> p.block_log2;
-    const float* ksc = p.k_scale + (size_t)b * nb * p.n_kv + h;
-    const float* vsc = p.v_scale + (size_t)b * nb * p.n_kv + h;
     // Eight neighbouring threads take four pieces of two rows: their 16-byte
     // stores, two pieces apart in a row and swizzled by the row, hit every bank once.
     const int tr = HD == 128 ? (t >> 4) * 2 + ((t >> 2) & 1) : t / CPR;
     const int tc = HD == 128 ? (t & 3) + ((t >> 3) & 1) * 4 : t % CPR;
+    const size_t base = (size_t)b * p.N * width + (size_t)h * HD + tc * 16;
+    // lanes 0-3: the key scales of the tile's 16-key groups, lanes 4-7 the value scales (1 past the length)
+    const float* scp = (lane & 4 ? p.v_scale : p.k_scale) + (size_t)b * nb * p.n_kv + h;
+    auto scale_of = [&](int j) {
+      const int key = (kt0 + j) * kTK + (lane & 3) * 16;
+      return j < n && key < len ? __ldg(scp + (size_t)(key >> p.block_log2) * p.n_kv) : 1.f;
+    };
     // the swizzle depends on row % 8, which the steps of ROWS rows leave alone
-    const int off = (tc >> 2) * 16384 + tr * 128, x7 = tr & 7;
+    const int off = (tc >> 2) * HALF + tr * 128, x7 = tr & 7;
     const int off0 = off + ((((tc & 3) * 2) ^ x7) << 4), off1 = off + ((((tc & 3) * 2 + 1) ^ x7) << 4);
-    // half u: K (u even) or V (u odd) of tile u / 2; its codes are loaded while half u - 1 is converted
-    uint4 r[PER];
-    auto fetch = [&](int u) {
-      const uint8_t* base = (u & 1 ? vbase : kbase) + tc * 16;
-      const int key0 = (kt0 + (u >> 1)) * kTT + tr;
+    uint4 kr[PER], vr[PER];
+    auto fetch = [&](const uint8_t* codes, int j, uint4 (&x)[PER]) {
+      const int key0 = (kt0 + j) * kTK + tr;
+      const uint8_t* src = codes + base + (size_t)key0 * width;
 #pragma unroll
       for (int it = 0; it < PER; ++it) {
-        const int key = key0 + it * ROWS;
-        r[it] = make_uint4(0u, 0u, 0u, 0u);
-        if (key < len)  // rows past the length are zeros, whatever the cache holds there
-          r[it] = __ldg(reinterpret_cast<const uint4*>(base + (size_t)key * width));
+        x[it] = make_uint4(0u, 0u, 0u, 0u);
+        if (j < n && key0 + it * ROWS < len)  // rows past the length are zeros, whatever the cache holds there
+          x[it] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)(it * ROWS) * width));
       }
     };
-    // bits g and 8 + g: 16-key group g of tile j has a key or a value scale of 0
-    auto zero_groups = [&](int j) {
-      const int key = (kt0 + j) * kTT + (lane & 7) * 16;
-      const bool z = j < n && key < len && __ldg((lane & 8 ? vsc : ksc) + (size_t)(key >> p.block_log2) * p.n_kv) == 0.f;
-      return __ballot_sync(0xffffffffu, z);
-    };
-    uint32_t zero = 0, zero_next = zero_groups(0);
-    if (n > 0) fetch(0);
-#pragma unroll 1
-    for (int u = 0; u < 2 * n; ++u) {
-      const int j = u >> 1, st = (u & 1) * 2 + (j & 1);
-      if (!(u & 1)) {
-        zero = zero_next;
-        zero_next = zero_groups(j + 1);
-      }
-      if (j >= 2 && !mbar_wait_clk(&sy.kv_empty[st], ((j >> 1) - 1) & 1, &sy.abort, err, 734)) break;
+    auto put = [&](int st, uint4 (&x)[PER], uint32_t zero) {
       uint8_t* tile = sK + st * Cfg::kTile;
-      if (zero & 0xFFu) {
+      if (zero) {  // a block whose scale is 0
 #pragma unroll
         for (int it = 0; it < PER; ++it)
-          if ((zero >> ((it * ROWS + tr) >> 4)) & 1) r[it] = make_uint4(0u, 0u, 0u, 0u);
+          if ((zero >> ((it * ROWS + tr) >> 4)) & 1) x[it] = make_uint4(0u, 0u, 0u, 0u);
       }
-      zero >>= 8;
 #pragma unroll
       for (int it = 0; it < PER; ++it) {
         uint4 lo, hi;
-        convert16<FMT>(r[it], lo, hi);
+        convert16<FMT>(x[it], lo, hi);
         *reinterpret_cast<uint4*>(tile + off0 + it * ROWS * 128) = lo;
         *reinterpret_cast<uint4*>(tile + off1 + it * ROWS * 128) = hi;
       }
       proxy_fence_smem();
       mbar_arrive_cta(&sy.kv_full[st]);
-      if (u + 1 < 2 * n) fetch(u + 1);
+    };
+    float sc_next = scale_of(0);
+    fetch(p.k_codes, 0, kr);
+    fetch(p.v_codes, 0, vr);
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const int st = j & 3;
+      const uint32_t ph = ((j >> 2) - 1) & 1;
+      // A key scale, times log2 e / sqrt(hd), goes to the scores; a value
+      // scale becomes the summand log2 vs of the exponent, and the row sum
+      // takes the group's sum times 1 / vs.  A scale of 0 counts as 1 (its
+      // codes are converted to zeros).
+      const float sc = sc_next == 0.f ? 1.f : sc_next, lg = lg2(sc);
+      const uint32_t zero = __ballot_sync(0xffffffffu, sc_next == 0.f);
+      if (t < 8) s_sc[j & 7][t] = t < 4 ? sc * p.scale_log2 : lg;
+      if (t >= 4 && t < 8) s_sc[j & 7][t + 4] = ex2(-lg);
+      sc_next = scale_of(j + 1);
+      if (j >= 4 && !mbar_wait_clk(&sy.kv_empty[st], ph, &sy.abort, err, 734)) break;
+      put(st, kr, zero & 15u);
+      fetch(p.k_codes, j + 1, kr);
+      if (j >= 4 && !mbar_wait_clk(&sy.kv_empty[4 + st], ph, &sy.abort, err, 735)) break;
+      put(4 + st, vr, (zero >> 4) & 15u);
+      fetch(p.v_codes, j + 1, vr);
     }
   } else {
     // ---------------------------------------------------------------- MMA
-    // The whole warp runs the loop and one elected lane issues, so that
-    // addresses and descriptors stay in uniform registers.
-    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128);
-    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, HD) | (1u << 16);  // V is MN-major
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t dq = smem_desc_sw128(smem_u32(sQ));
-    const uint64_t dk = smem_desc_sw128(smem_u32(sK));
-    const uint64_t dv = desc_sw128_mn(smem_u32(sV), 16384);
-    constexpr uint64_t kTileOff = Cfg::kTile >> 4, kQOff = Cfg::kQBytes >> 4;
-    bool ok = n > 0 && mma_wait(&sy.q_full, 0, &sy.abort, err, 736);
+    // One thread per query tile i: its waits do not hold up the other tile's MMAs.
+    const int i = warp - kMmaWarp;
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kTK);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, HD) | (1u << 16);  // V is MN-major
+      constexpr uint64_t kTileOff = Cfg::kTile >> 4;
+      const uint64_t dq = smem_desc_sw128(smem_u32(sQ + i * Cfg::kQBytes));
+      const uint64_t dk = smem_desc_sw128(smem_u32(sK));
+      const uint64_t dv = desc_sw128_mn(smem_u32(sV), kTK * 128);
+      const uint32_t ts = tmem + (uint32_t)(i * 128), to = tmem + 256u + (uint32_t)(i * 128);
+      const bool ok = n > 0 && mbar_wait_clk(&sy.q_full, 0, &sy.abort, err, 736);
+      // step j: PV of tile j - 2 (from j = 2), QK^T of tile j (to j = n - 1); they share a score buffer
 #pragma unroll 1
-    for (int j = 0; ok && j <= n; ++j) {
-      const int st = j & 1, pst = st ^ 1;
-      if (j < n && !mma_wait(&sy.kv_full[st], (j >> 1) & 1, &sy.abort, err, 737)) break;
-      if (j > 0 && !mma_wait(&sy.kv_full[2 + pst], ((j - 1) >> 1) & 1, &sy.abort, err, 738)) break;
-#pragma unroll 1
-      for (int i = 0; i < NQ; ++i) {
-        if (j > 0) {
-          if (!mma_wait(&sy.p_full[i], (j - 1) & 1, &sy.abort, err, 739)) { ok = false; break; }
+      for (int j = 0; ok && j < n + 2; ++j) {
+        const int st = j & 3, pj = j - 2, pst = pj & 3, sb = j & 1;
+        if (pj >= 0 && pj < n) {
+          if (!mbar_wait_clk(&sy.kv_full[4 + pst], (pj >> 2) & 1, &sy.abort, err, 738)) break;
+          if (!mbar_wait_clk(&sy.p_full[2 * i + sb], (pj >> 1) & 1, &sy.abort, err, 739)) break;
           tc_fence_after();
-          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_bf16_ts(tm + 256u + i * 128u, tm + i * 128u + kk * 8u, dv + pst * kTileOff + (uint64_t)(kk * 128),
-                           idesc_pv, (j > 1 || kk > 0) ? 1u : 0u);
-            if (i == NQ - 1) umma_commit(&sy.kv_empty[2 + pst]);
-          }
+          for (int kk = 0; kk < kTK / 16; ++kk)
+            umma_bf16_ts(to, ts + sb * 64u + kk * 8u, dv + pst * kTileOff + (uint64_t)(kk * 128), idesc_pv,
+                         (pj > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&sy.pv_done[i]);
+          umma_commit(&sy.kv_empty[4 + pst]);
         }
         if (j < n) {
+          if (!mbar_wait_clk(&sy.kv_full[st], (j >> 2) & 1, &sy.abort, err, 737)) break;
           tc_fence_after();
-          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-              const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);
-              umma_bf16(tm + i * 128u, dq + i * kQOff + off, dk + st * kTileOff + off, idesc_qk, kk > 0 ? 1u : 0u);
-            }
-            umma_commit(&sy.s_full[i]);
-            if (i == NQ - 1) umma_commit(&sy.kv_empty[st]);
-          }
+          for (int kk = 0; kk < HD / 16; ++kk)
+            umma_bf16(ts + sb * 64u, dq + (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2),
+                      dk + st * kTileOff + (uint64_t)((kk >> 2) * (kTK * 8) + (kk & 3) * 2), idesc_qk, kk > 0 ? 1u : 0u);
+          umma_commit(&sy.s_full[2 * i + sb]);
+          umma_commit(&sy.kv_empty[st]);
         }
       }
+      umma_commit(&sy.o_done);
     }
-    __syncwarp();
-    if (elect_one()) umma_commit(&sy.o_done);
   }
   __syncwarp();
   __syncthreads();
@@ -572,15 +560,15 @@ static cudaError_t launch_tc(Q8AttnParams& p, int splits_most, cudaStream_t stre
 }
 
 // Key shares: doubled while the grid stays within the SMs (one CTA on each,
-// by shared memory) and every share keeps a tile.
+// by shared memory) and every share keeps two tiles.
 static int tc_splits(long long ctas, int n_kt, int num_sms) {
   int s = 1;
-  while (s < 8 && ctas * s * 2 <= num_sms && n_kt >= s * 2) s *= 2;
+  while (s < 8 && ctas * s * 2 <= num_sms && n_kt >= s * 4) s *= 2;
   return s;
 }
 
 cudaError_t launch_q8_attention_tc(int fmt, int hd, Q8AttnParams p, int num_sms, cudaStream_t stream) {
-  const int n_kt = (p.N + kTT - 1) / kTT;
+  const int n_kt = (p.N + kTK - 1) / kTK;
   const long long heads = (long long)p.B * p.n_kv;
   const int t1 = (p.k * p.group + kTT - 1) / kTT, t2 = (t1 + 1) / 2;
   // two query tiles in a CTA share the converted keys and values; one while the single tiles do not fill the SMs
