@@ -15,10 +15,11 @@
 //                   the TMEM operand, so P never touches shared memory
 // Two score buffers of 64 keys each let the softmax of a query tile go from
 // one key tile to the next without waiting for PV and the next QK^T (one
-// buffer of 128 keys: 225 against XX us for k = 512 of N = 2048, B = 8,
+// buffer of 128 keys: 225 against 215 us for k = 512 of N = 2048, B = 8,
 // 32 heads of 128; a QK^T of 64 keys costs 48 cycles a step where 32 would be
-// half of one of 128).  MMAs of one thread execute in order, so QK_i(j + 2)
-// overwrites P_i(j) after PV_i(j) has read it.
+// half of one of 128).  QK_i(j + 2), which overwrites P_i(j), is issued once
+// PV_i(j) has completed: two tiles ahead of its softmax, so that the wait
+// costs nothing.
 //
 // The scales stay out of the conversion: a key block's multiplies its scores
 // in the product the softmax makes anyway, a value block's becomes a summand
@@ -45,13 +46,15 @@ template <int HD, int NQ> struct TcCfg {
   static constexpr int kStages = 4;                   // K ring, V ring
   static constexpr int kThreads = NQ * 128 + 128 + NQ * 32;
   static constexpr int kUsed = NQ * kQBytes + 2 * kStages * kTile + 1024;
-  // at least 120 KB, so that no SM holds two CTAs that want its tensor memory
-  static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+  // at least 132 KB, so that no SM holds a second CTA that wants its tensor
+  // memory: another of these, or a GEMM's (99 KB or more)
+  static constexpr int kSmem = kUsed > 132 * 1024 ? kUsed : 132 * 1024;
 };
 
 struct TcSync {
   uint64_t q_full, kv_full[8], kv_empty[8], o_done;  // K stages 0-3, V stages 4-7
   uint64_t s_full[4], p_full[4], pv_done[2];         // [2 * query tile + score buffer], [query tile]
+  uint64_t sc_full[8];                               // the scales of a key tile
   uint32_t tmem;
   int abort, ok;
 };
@@ -169,6 +172,7 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
   if (tid == 0) {
     mbar_init(&sy.q_full, NQ * 128);
     for (int s = 0; s < 8; ++s) {
+      mbar_init(&sy.sc_full[s], 1);
       mbar_init(&sy.kv_full[s], 128);
       mbar_init(&sy.kv_empty[s], NQ);
     }
@@ -238,14 +242,14 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
     bool ok = true;
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      const bool got = mbar_wait_clk(&sy.s_full[2 * i + (j & 1)], (j >> 1) & 1, &sy.abort, err, 732);
+      const bool got = mbar_wait_clk(&sy.sc_full[j & 7], (j >> 3) & 1, &sy.abort, err, 742) &&
+                       mbar_wait_clk(&sy.s_full[2 * i + (j & 1)], (j >> 1) & 1, &sy.abort, err, 732);
       __syncwarp();
       if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
       tc_fence_after();
       const uint32_t s_at = s_base + (uint32_t)((j & 1) * kTK);
       uint32_t x[kTK];
       load_scores(s_at, x, len - (kt0 + j) * kTK);
-      // written by the conversion warps before the tile whose scores these are
       const float4 a4 = *reinterpret_cast<const float4*>(s_sc[j & 7]), lv4 = *reinterpret_cast<const float4*>(s_sc[j & 7] + 4);
       const float4 rv4 = *reinterpret_cast<const float4*>(s_sc[j & 7] + 8);
       const float a[4] = {a4.x, a4.y, a4.z, a4.w}, lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
@@ -422,6 +426,8 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
       const uint32_t zero = __ballot_sync(0xffffffffu, sc_next == 0.f);
       if (t < 8) s_sc[j & 7][t] = t < 4 ? sc * p.scale_log2 : lg;
       if (t >= 4 && t < 8) s_sc[j & 7][t + 4] = ex2(-lg);
+      __syncwarp();
+      if (t == 0) mbar_arrive_cta(&sy.sc_full[j & 7]);  // slot j % 8: both softmaxes are past tile j - 8 by now
       sc_next = scale_of(j + 1);
       if (j >= 4 && !mbar_wait_clk(&sy.kv_empty[st], ph, &sy.abort, err, 734)) break;
       put(st, kr, zero & 15u);
@@ -460,6 +466,7 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
         }
         if (j < n) {
           if (!mbar_wait_clk(&sy.kv_full[st], (j >> 2) & 1, &sy.abort, err, 737)) break;
+          if (pj >= 0 && !mbar_wait_clk(&sy.pv_done[i], pj & 1, &sy.abort, err, 743)) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk)

@@ -385,22 +385,20 @@ class Model:
 
 # --------------------------------------------------- 8-bit K/V cache, log probabilities
 
-def _arg(t, name: str, shape, dtype, device=None, rows_strided=False):
-    """Checks a tensor argument whose layout the C ABI cannot see."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _arg(t, name: str, n: int, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of n elements on CUDA device `dev`, the layout the C ABI cannot see."""
+    try:
+        if t.dtype is dtype and t.numel() == n and t.get_device() == dev >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise ValueError(f"{name} must be a CUDA tensor") from None
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call is for CUDA device {dev}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    n = 1
-    for s in shape:
-        n *= s
     if t.numel() != n:
-        raise ValueError(f"{name} must hold {tuple(shape)}, not {tuple(t.shape)}")
-    if not rows_strided and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+        raise ValueError(f"{name} must hold {n} elements, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 class Q8Cache:
@@ -423,54 +421,53 @@ class Q8Cache:
         self.B, self.N, self.n_kv_heads, self.head_dim, self.block, self.fmt = B, N, n_kv_heads, head_dim, block, fmt
         self.desc = Q8CacheDesc(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
                                 self.v_scale.data_ptr(), B, N, n_kv_heads, head_dim, block, fmt)
+        self.ref = ctypes.byref(self.desc)
+        self.dev = self.k.get_device()
 
 
 def spa_q8_write(ws: Workspace, cache: Q8Cache, k_rows, v_rows, idx=None, indexed: bool = False, stream=None):
     """Writes k_rows, v_rows [B, k, n_kv_heads * head_dim] into rows idx [B, k] (None: 0..k-1) of the cache;
     with indexed, the rows idx of k_rows, v_rows [B, N, n_kv_heads * head_dim]."""
-    dt, dev, w = torch_dtype(ws.desc.dtype), cache.k.device, cache.n_kv_heads * cache.head_dim
+    dt, B, dev, w = torch_dtype(ws.desc.dtype), cache.B, cache.dev, cache.n_kv_heads * cache.head_dim
+    ip = None
     if idx is not None:
-        k = idx.numel() // cache.B
-        _arg(idx, "idx", (cache.B, k), torch.int32, dev)
+        k = idx.numel() // B
+        ip = _arg(idx, "idx", B * k, torch.int32, dev)
     else:
-        k = cache.N if indexed else k_rows.numel() // (cache.B * w)
-    n = cache.N if indexed else k
-    kp = _arg(k_rows, "k_rows", (cache.B, n, w), dt, dev)
-    vp = _arg(v_rows, "v_rows", (cache.B, n, w), dt, dev)
-    _check(lib.spa_q8_write(ws.handle, ctypes.byref(cache.desc), kp, vp, int(indexed), _ptr(idx), k,
-                            _stream(stream)), "spa_q8_write")
+        k = cache.N if indexed else k_rows.numel() // (B * w)
+    n = B * (cache.N if indexed else k) * w
+    _check(lib.spa_q8_write(ws.handle, cache.ref, _arg(k_rows, "k_rows", n, dt, dev), _arg(v_rows, "v_rows", n, dt, dev),
+                            int(indexed), ip, k, _stream(stream)), "spa_q8_write")
 
 
 def spa_q8_read(ws: Workspace, cache: Q8Cache, k_out, v_out, idx=None, stream=None):
     """Values of rows idx [B, k] (None: 0..k-1) into k_out, v_out [B, k, n_kv_heads * head_dim]."""
-    dt, dev, w = torch_dtype(ws.desc.dtype), cache.k.device, cache.n_kv_heads * cache.head_dim
-    k = k_out.numel() // (cache.B * w)
-    if idx is not None:
-        _arg(idx, "idx", (cache.B, k), torch.int32, dev)
-    kp = _arg(k_out, "k_out", (cache.B, k, w), dt, dev)
-    vp = _arg(v_out, "v_out", (cache.B, k, w), dt, dev)
-    _check(lib.spa_q8_read(ws.handle, ctypes.byref(cache.desc), _ptr(idx), k, kp, vp, _stream(stream)),
-           "spa_q8_read")
+    dt, B, dev, w = torch_dtype(ws.desc.dtype), cache.B, cache.dev, cache.n_kv_heads * cache.head_dim
+    k = k_out.numel() // (B * w)
+    ip = None if idx is None else _arg(idx, "idx", B * k, torch.int32, dev)
+    n = B * k * w
+    _check(lib.spa_q8_read(ws.handle, cache.ref, ip, k, _arg(k_out, "k_out", n, dt, dev),
+                           _arg(v_out, "v_out", n, dt, dev), _stream(stream)), "spa_q8_read")
 
 
 def spa_q8_attention(ws: Workspace, Q, cache: Q8Cache, O, lens=None, stream=None):
     """O = attention of Q [B, k, n_heads * head_dim] over the first lens [B] rows (None: all) of the cache."""
-    dt, dev, d = torch_dtype(ws.desc.dtype), cache.k.device, ws.desc.d
-    k = Q.numel() // (cache.B * d)
-    qp = _arg(Q, "Q", (cache.B, k, d), dt, dev)
-    op = _arg(O, "O", (cache.B, k, d), dt, dev)
-    lp = None if lens is None else _arg(lens, "lens", (cache.B,), torch.int32, dev)
-    _check(lib.spa_q8_attention(ws.handle, qp, ctypes.byref(cache.desc), lp, op, k, _stream(stream)),
-           "spa_q8_attention")
+    desc, B, dev = ws.desc, cache.B, cache.dev
+    dt, d = torch_dtype(desc.dtype), desc.d
+    k = Q.numel() // (B * d)
+    n = B * k * d
+    lp = None if lens is None else _arg(lens, "lens", B, torch.int32, dev)
+    _check(lib.spa_q8_attention(ws.handle, _arg(Q, "Q", n, dt, dev), cache.ref, lp, _arg(O, "O", n, dt, dev), k,
+                                _stream(stream)), "spa_q8_attention")
 
 
 def spa_layer_step_q8(layer: Layer, H, cache: Cache, q8: Q8Cache, k: int, idx, stream=None):
-    _check(lib.spa_layer_step_q8(layer.handle, _ptr(H), ctypes.byref(cache.desc), ctypes.byref(q8.desc), k,
+    _check(lib.spa_layer_step_q8(layer.handle, _ptr(H), ctypes.byref(cache.desc), q8.ref, k,
                                  _ptr(idx), _stream(stream)), "spa_layer_step_q8")
 
 
 def spa_full_block_q8(layer: Layer, H, cache: Cache, q8: Q8Cache, fill_proxy: int = 1, stream=None):
-    _check(lib.spa_full_block_q8(layer.handle, _ptr(H), ctypes.byref(cache.desc), ctypes.byref(q8.desc),
+    _check(lib.spa_full_block_q8(layer.handle, _ptr(H), ctypes.byref(cache.desc), q8.ref,
                                  int(fill_proxy), _stream(stream)), "spa_full_block_q8")
 
 
@@ -495,18 +492,20 @@ def spa_token_logprobs(ws: Workspace, logits, tok, logp, entropy, top_id=None, t
         raise ValueError("logits must not be empty")
     if (vocab > 1 and logits.stride(1) != 1) or (rows > 1 and logits.stride(0) < vocab):
         raise ValueError("logits must be contiguous along the vocabulary, with rows that do not overlap")
-    dev = logits.device
-    lp = _arg(logits, "logits", (rows, vocab), logits.dtype, dev, rows_strided=True)
-    top = 0 if top_id is None else top_id.numel() // rows
-    args = [_arg(tok, "tok", (rows,), torch.int32, dev), top, _arg(logp, "logp", (rows,), torch.float32, dev),
-            _arg(entropy, "entropy", (rows,), torch.float32, dev)]
-    if top:
-        args += [_arg(top_id, "top_id", (rows, top), torch.int32, dev),
-                 _arg(top_logp, "top_logp", (rows, top), torch.float32, dev)]
-    else:
-        args += [None, None]
-    _check(lib.spa_token_logprobs(ws.handle, lp, SPA_BF16 if logits.dtype == torch.bfloat16 else SPA_F32, rows, vocab,
-                                  logits.stride(0) if rows > 1 else vocab, *args, _stream(stream)),
+    dev = logits.get_device()
+    if dev < 0:
+        raise ValueError("logits must be a CUDA tensor")
+    top, ip, vp = 0, None, None
+    if top_id is not None:
+        top = top_id.numel() // rows
+        if top:
+            ip = _arg(top_id, "top_id", rows * top, torch.int32, dev)
+            vp = _arg(top_logp, "top_logp", rows * top, torch.float32, dev)
+    _check(lib.spa_token_logprobs(ws.handle, logits.data_ptr(), SPA_BF16 if logits.dtype is torch.bfloat16 else SPA_F32,
+                                  rows, vocab, logits.stride(0) if rows > 1 else vocab,
+                                  _arg(tok, "tok", rows, torch.int32, dev), top,
+                                  _arg(logp, "logp", rows, torch.float32, dev),
+                                  _arg(entropy, "entropy", rows, torch.float32, dev), ip, vp, _stream(stream)),
            "spa_token_logprobs")
 
 
