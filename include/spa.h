@@ -320,8 +320,8 @@ int spa_model_set_incremental_proxy(spa_model *model, int enable);
  * byte each, int8 in -127..127 (SPA_Q8_INT8) or e4m3 (SPA_Q8_E4M3, whose NaN
  * codes do not occur), 16-byte aligned; scales [B, ceil(N / block),
  * n_kv_heads] float, one for each `block` tokens of a head (the last block
- * may be cut by N).  A value is its code times its scale.  Start with all
- * bytes of the four buffers zero.  head_dim is 32, 64 or 128 and that of the
+ * may be cut by N), not negative.  A value is its code times its scale.
+ * Start with all bytes of the four buffers zero.  head_dim is 32, 64 or 128 and that of the
  * workspace's layer descriptor; n_kv_heads divides its n_heads (query head h
  * reads kv head h / (n_heads / n_kv_heads)); rows passed to and from the
  * calls have the descriptor's dtype. */
@@ -350,8 +350,8 @@ int spa_q8_write(spa_workspace *ws, const spa_q8_cache *cache, const void *k_row
                  int indexed, const int32_t *idx, int k, void *stream);
 /* Reads rows back: k_out / v_out [B, k, n_kv_heads * head_dim] (16-byte
  * aligned) receive the values of rows idx[b, i] ([B, k] int32 device; NULL:
- * rows 0..k-1, k <= N), exact in bf16 and fp32 for the scales spa_q8_write
- * makes.  The output row of an index outside [0, N) is left as it was and
+ * rows 0..k-1, k <= N), rounded to the type (no rounding for the scales
+ * spa_q8_write makes, bf16's subnormal range apart).  The output row of an index outside [0, N) is left as it was and
  * reported. */
 int spa_q8_read(spa_workspace *ws, const spa_q8_cache *cache, const int32_t *idx, int k, void *k_out,
                 void *v_out, void *stream);
@@ -360,8 +360,8 @@ int spa_q8_read(spa_workspace *ws, const spa_q8_cache *cache, const int32_t *idx
  * and reported): Q, O [B, k, n_heads * head_dim], the descriptor's dtype,
  * 16-byte aligned and not overlapping, k >= 1 queries per sequence.  A sequence of length 0 gives zeros.  Cache rows
  * past the length are not read into the result, whatever they hold.  Scores,
- * softmax statistics and sums are fp32; with bf16 queries the probabilities
- * are rounded to bf16 before the product with V, as in spa_partial_block. */
+ * softmax statistics and sums are fp32; with bf16 queries a probability is
+ * rounded to 8 or 11 significant bits before its product with V. */
 int spa_q8_attention(spa_workspace *ws, const void *Q, const spa_q8_cache *cache, const int32_t *lens,
                      void *O, int k, void *stream);
 

@@ -368,6 +368,48 @@ def test_attention_ignores_what_lies_past_the_length(hd, k):
     assert torch.count_nonzero(clean[2]) == 0
 
 
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dtype,k", [(BF16, 1), (BF16, 130), (F32, 1)])
+def test_every_code_comes_through(fmt, dtype, k):
+    """One key: the output is the value row, so every code (subnormal ones too) has to come out as it is."""
+    heads, hd = 2, 128
+    ws = make_ws(dtype, heads, hd, 1, 16)
+    cache = spa.Q8Cache(1, 1, heads, hd, block=16, fmt=fmt)
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8)
+    if fmt == E4M3:
+        codes[127], codes[255] = 0, 0           # the two NaN codes
+    else:
+        codes[128] = 129                        # -128 is no code
+    cache.v.view(torch.uint8).copy_(codes.view(1, 1, 256).cuda())
+    cache.k.view(torch.uint8).copy_(codes.flip(0).view(1, 1, 256).cuda())
+    cache.k_scale.fill_(2.0 ** -4)
+    cache.v_scale.fill_(2.0 ** 3)
+    q = torch.randn((1, k, heads, hd), device="cuda").to(spa.torch_dtype(dtype))
+    out = run_attention(ws, cache, q)
+    ws.check()
+    V, _ = device_values(cache, "v")
+    assert np.array_equal(np64(out), np.broadcast_to(V, (1, k, heads, hd)))
+    got = [torch.empty((1, 1, heads * hd), dtype=spa.torch_dtype(dtype), device="cuda") for _ in range(2)]
+    spa.spa_q8_read(ws, cache, got[0], got[1])
+    assert np.array_equal(np64(got[1]).reshape(V.shape), V)
+
+
+@pytest.mark.parametrize("k", [1, 150])
+def test_attention_with_scales_that_are_no_powers_of_two(k):
+    """A cache another program has quantised (max / qmax scales) is read as it is."""
+    rng = np.random.default_rng(12)
+    B, N, heads, hd = 1, 300, 2, 128
+    ws = make_ws(BF16, heads, hd, B, N)
+    cache = spa.Q8Cache(B, N, heads, hd, block=32, fmt=INT8)
+    fill_cache(rng, cache)
+    cache.k_scale.copy_(torch.from_numpy((0.003 + 0.01 * rng.random(cache.k_scale.shape)).astype(np.float32)))
+    cache.v_scale.copy_(torch.from_numpy((0.01 + 10.0 * rng.random(cache.v_scale.shape) ** 8).astype(np.float32)))
+    q = torch.from_numpy(rng.standard_normal((B, k, heads, hd)).astype(np.float32)).to(torch.bfloat16).cuda()
+    out = run_attention(ws, cache, q)
+    ref, bound = ref_attention(np64(q), cache, [N], heads, False)
+    assert np.all(np.abs(np64(out) - ref) <= bound)
+
+
 def test_attention_lengths_outside_are_clamped_and_reported():
     rng = np.random.default_rng(9)
     ws = make_ws(BF16, 2, 128, 2, 64)
@@ -612,6 +654,32 @@ def test_decode_over_8_bit_caches_with_log_probabilities(inc):
             ws.check()
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,vocab,B,N", [(BF16, 1003, 2, 160), (BF16, 1024, 2, 160), (BF16, 130, 1, 40), (F32, 1001, 1, 64)])
+def test_logits_of_many_and_few_positions(dtype, vocab, B, N):
+    """spa_decode_logits at every position (more than 256 rows and fewer), odd vocabularies, and the rest of the
+    buffer left as it was."""
+    shape = SHAPE if dtype == BF16 else synth.TINY_LAYER
+    lp = LayerPair(spa, shape, seed=97, dtype=dtype, max_B=B, max_N=N, std=0.05)
+    tdt = spa.torch_dtype(dtype)
+    embed, lm = (torch.randn((vocab, shape.d), device="cuda").to(tdt) for _ in range(2))
+    ones = torch.ones((shape.d,), device="cuda").to(tdt)
+    h0 = torch.zeros((B, N, shape.d), dtype=tdt, device="cuda")
+    cache = lp.cache(B, N)
+    model = spa.Model([lp.layer], [cache], h0, embed, ones, lm, vocab, B, N, 0.25, 1, 0.25, 0.25)
+    model.embed_tokens(torch.randint(0, vocab, (B, N), dtype=torch.int32, device="cuda"))
+    spa.spa_decode_layers(model, 1)
+    pos = torch.arange(N, dtype=torch.int32, device="cuda").repeat(B, 1)
+    buf = torch.full((B * N + 1, vocab), -7.0, device="cuda")
+    spa.spa_decode_logits(model, pos, N, buf)
+    lp.ws.check()
+    rows = np64(cache.h).reshape(B * N, shape.d)
+    x = rows / np.sqrt((rows ** 2).mean(-1, keepdims=True) + shape.rms_eps)
+    if dtype == BF16:
+        x = np64(torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16))
+    assert_close(buf[:-1], x @ np64(lm).T, dtype == BF16, "logits")
+    assert torch.all(buf[-1] == -7.0)
 
 
 def test_changing_the_cache_drops_a_captured_graph():
