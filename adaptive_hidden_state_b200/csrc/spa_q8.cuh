@@ -82,6 +82,18 @@ template <int FMT> __device__ __forceinline__ uint32_t q8_pair_f16(uint32_t x, u
   }
 }
 
+// Asynchronous copies to shared memory; bytes 0: zeros, src is not read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // One code as float.
 template <int FMT> __device__ __forceinline__ float q8_value(uint32_t byte) {
   if constexpr (FMT == kQ8Int8) return (float)(int8_t)(uint8_t)byte;

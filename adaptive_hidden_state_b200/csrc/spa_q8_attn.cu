@@ -57,17 +57,6 @@ template <int HD> struct RowCfg {
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Byte offset of 16-byte piece c of row r (rows of HD bytes).
 template <int HD> __device__ __forceinline__ int row_piece(int r, int c) {
   constexpr int RPL = 128 / HD, CPR = HD / 16, MUL = HD == 128 ? 1 : 2;

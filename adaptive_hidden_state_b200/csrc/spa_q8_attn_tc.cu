@@ -224,15 +224,15 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
       return qtile + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
     };
     {
-      uint4 v[CPR];
+      // asynchronous copies: all of a thread's pieces in flight, none in registers
 #pragma unroll
       for (int it = 0; it < CPR; ++it) {
         const long long o = __shfl_sync(0xffffffffu, my_off, it * RPI + lane / CPR);
-        v[it] = make_uint4(0u, 0u, 0u, 0u);
-        if (o >= 0) v[it] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.Q) + o) + lane % CPR);
+        cp_async16(smem_u32(piece(it)), reinterpret_cast<const __nv_bfloat16*>(p.Q) + (o >= 0 ? o : 0) + (lane % CPR) * 8,
+                   o >= 0 ? 16 : 0);
       }
-#pragma unroll
-      for (int it = 0; it < CPR; ++it) *reinterpret_cast<uint4*>(piece(it)) = v[it];
+      cp_async_commit();
+      cp_async_wait<0>();
       proxy_fence_smem();
       mbar_arrive_cta(&sy.q_full);
     }
