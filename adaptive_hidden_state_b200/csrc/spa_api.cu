@@ -1052,7 +1052,6 @@ static int run_q8_attention(spa_workspace* ws, const void* Q, const spa_q8_cache
   p.Q = Q; p.O = O; p.lens = lens;
   p.k_codes = (const uint8_t*)c->k_codes; p.v_codes = (const uint8_t*)c->v_codes;
   p.k_scale = c->k_scale; p.v_scale = c->v_scale;
-  p.sync = ws->attn_sync;
   p.err = ws->err;
   p.B = c->B; p.k = k; p.N = c->N; p.n_heads = D.n_heads; p.n_kv = c->n_kv_heads;
   p.group = D.n_heads / c->n_kv_heads;
@@ -1061,7 +1060,7 @@ static int run_q8_attention(spa_workspace* ws, const void* Q, const spa_q8_cache
   const double q = 2.0 * c->B * k * D.d * (bf ? 2 : 4), kv = 2.0 * c->B * c->N * c->n_kv_heads * c->head_dim;
   ProfScope ps(&ws->prof, SPA_PROF_ATTN, q + kv, 4.0 * c->B * k * D.d * c->N, s);
   const cudaError_t e = launch_q8_attention(bf, c->format, D.head_dim, p, ws->part_o, (size_t)ws->part_rows * D.d,
-                                            ws->attn_sync_len, ws->num_sms, s);
+                                            ws->num_sms, s);
   if (e != cudaSuccess) return fail(SPA_ERR_CUDA, "8-bit cache attention launch: %s", cudaGetErrorString(e));
   return SPA_OK;
 }

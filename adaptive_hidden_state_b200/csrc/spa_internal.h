@@ -299,7 +299,6 @@ struct Q8AttnParams {
   const float *k_scale, *v_scale;
   const int32_t* lens;          // [B] rows of each sequence that count (null: N)
   float *part_o, *part_ml;      // key shares: unnormalised rows, (m, l) pairs
-  int* sync;                    // arrivals per row tile, zero between launches
   int* err;
   int B, k, N, n_heads, n_kv, group, block_log2, tiles, splits;
   float scale_log2;             // log2(e) / sqrt(hd)
@@ -308,11 +307,12 @@ struct Q8AttnParams {
 cudaError_t launch_q8_write(int dtype, int fmt, int block, Q8WriteParams p, int num_sms,
                             cudaStream_t stream);
 cudaError_t launch_q8_read(int dtype, int fmt, int block, Q8ReadParams p, cudaStream_t stream);
-// part: scratch for the key shares, sync: [sync_len] ints, zero between launches.
+// part: scratch for the key shares.
 cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, float* part, size_t part_floats,
-                                size_t sync_len, int num_sms, cudaStream_t stream);
+                                int num_sms, cudaStream_t stream);
 // The tensor-core kernel for many query rows (bf16, hd 64 or 128).
 cudaError_t launch_q8_attention_tc(int fmt, int hd, Q8AttnParams p, int num_sms, cudaStream_t stream);
+double q8_attention_tc_us(const Q8AttnParams& p, int hd, int num_sms);  // its estimated time
 // Per row of logits [rows, V] (row stride ld elements): log probability of
 // tok, entropy, and the `top` largest (ties to the lowest id).
 struct LogpParams {

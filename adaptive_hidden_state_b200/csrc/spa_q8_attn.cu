@@ -9,8 +9,9 @@
 // outside them: a key block's scale multiplies its scores, a value block's
 // scale the probabilities before they are rounded.
 //
-// q8_attn_rows_kernel (below) takes 16 query rows per CTA: single tokens, fp32
-// queries, head_dim 32.  More rows in bf16 go to spa_q8_attn_tc.cu.
+// q8_attn_rows_kernel (below) takes 16 query rows per CTA: few rows, fp32
+// queries, head_dim 32.  Many rows in bf16 go to spa_q8_attn_tc.cu.
+#include <cmath>
 #include <cstring>
 
 #include "spa_q8.cuh"
@@ -42,9 +43,11 @@ namespace spa {
 // fp32 queries: Q and P are each the sum of three f16 terms (24 bits and
 // more), so three products give the fp32 result to fp32 accuracy.
 //
-// The warps' results are joined in shared memory in warp order, and the key
-// shares of a row tile through global scratch by the last CTA to arrive, in
-// share order: the result does not depend on timing.
+// The warps' results are joined in shared memory in warp order, the key shares
+// of a row by a second small kernel, a CTA per row, in share order: the result
+// does not depend on timing.  (The last CTA of a row tile to arrive, joining
+// all of its rows alone: 36 against 13.6 us for one token over 16000 tokens, 2
+// kv heads, 64 shares.)
 // ---------------------------------------------------------------------------
 constexpr int kRWarps = 4, kRThreads = kRWarps * 32;
 constexpr int kRKeys = 32;    // keys of a chunk
@@ -100,7 +103,6 @@ __global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnPar
   constexpr int KW = HD / 16;                 // words of a key a thread reads = k16 steps of Q K^T
   constexpr int VB = HD / 8;                  // consecutive columns of V a thread reads = n8 tiles of P V
   constexpr int SB = RowCfg<HD>::kStageBytes;
-  __shared__ int s_last;
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
@@ -373,34 +375,66 @@ __global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnPar
       }
     }
   }
-  if (S == 1) return;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicAdd(p.sync + grp, 1) == S - 1;
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  for (int task = threadIdx.x; task < rows * (HD / 4); task += kRThreads) {
-    const int row = task / (HD / 4), col = (task % (HD / 4)) * 4;
-    float mm = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < S; ++s) mm = fmaxf(mm, __ldcg(p.part_ml + ((grp * S + s) * 16 + row) * 2));
-#pragma unroll 4
-    for (int s = 0; s < S; ++s) {
-      const size_t pr = (grp * S + s) * 16 + row;
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + pr * 2));
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + pr * HD + col));
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mm);
-      L += f * ml.y;
-      acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
-    }
-    const float inv = L != 0.f ? 1.0f / L : 0.f;
-    const int r = tile * 16 + row;
-    T* dst = reinterpret_cast<T*>(p.O) +
-             (((size_t)b * p.k + r / p.group) * p.n_heads + (size_t)h * p.group + r % p.group) * HD + col;
-    store4(dst, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+}
+
+// Row blockIdx.x of kv head blockIdx.y of sequence blockIdx.z from its S <= 64
+// key shares: each warp takes every fourth share (or pair, or four, of
+// narrower heads), then the warps are summed in order.
+template <typename T, int HD>
+__global__ void __launch_bounds__(kRThreads) q8_attn_join_kernel(const Q8AttnParams p) {
+  constexpr int COLS = HD / 4, SUB = 32 / COLS;
+  __shared__ float4 s_acc[kRWarps][COLS];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.x, S = p.splits;
+  const size_t grp = ((size_t)blockIdx.z * p.n_kv + blockIdx.y) * p.tiles + r / 16;
+  const size_t row0 = grp * S * 16 + r % 16;  // partial row of share 0; share s is 16 s further
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row0;
+  float2 a = make_float2(-INFINITY, 0.f), b = a;
+  if (lane < S) a = ml[16 * lane];
+  if (lane + 32 < S) b = ml[16 * (lane + 32)];
+  // this lane's columns of its shares, all loads in flight
+  constexpr int PER = 64 / (kRWarps * SUB);
+  const int col = lane % COLS, s0 = warp * SUB + lane / COLS;
+  float4 v[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int s = s0 + i * kRWarps * SUB;
+    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s < S) v[i] = *reinterpret_cast<const float4*>(p.part_o + (row0 + 16 * (size_t)s) * HD + col * 4);
   }
-  if (threadIdx.x == 0) p.sync[grp] = 0;  // ready for the next launch
+  const float mm = warp_max(fmaxf(a.x, b.x));
+  const float wa = a.x == -INFINITY && a.y == 0.f ? 0.f : exp2f(a.x - mm);  // a share without keys adds nothing
+  const float wb = b.x == -INFINITY && b.y == 0.f ? 0.f : exp2f(b.x - mm);
+  const float L = warp_sum(wa * a.y + wb * b.y);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int s = s0 + i * kRWarps * SUB;
+    const float w0 = __shfl_sync(0xffffffffu, wa, s & 31), w1 = __shfl_sync(0xffffffffu, wb, s & 31);
+    const float w = s < 32 ? w0 : w1;
+    acc.x = fmaf(w, v[i].x, acc.x); acc.y = fmaf(w, v[i].y, acc.y);
+    acc.z = fmaf(w, v[i].z, acc.z); acc.w = fmaf(w, v[i].w, acc.w);
+  }
+#pragma unroll
+  for (int o = COLS; o < 32; o <<= 1) {
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o); acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o); acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+  }
+  if (lane < COLS) s_acc[warp][lane] = acc;
+  __syncthreads();
+  if (threadIdx.x < COLS) {
+#pragma unroll
+    for (int w = 1; w < kRWarps; ++w) {
+      const float4 o = s_acc[w][threadIdx.x];
+      acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
+    }
+    const float inv = L != 0.f ? 1.0f / L : 0.f;  // no key: zeros
+    T* dst = reinterpret_cast<T*>(p.O) +
+             (((size_t)blockIdx.z * p.k + r / p.group) * p.n_heads + (size_t)blockIdx.y * p.group + r % p.group) * HD;
+    store4(dst + threadIdx.x * 4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  }
 }
 
 template <typename T, int HD, int FMT>
@@ -408,35 +442,55 @@ static cudaError_t launch_rows(const Q8AttnParams& p, cudaStream_t stream) {
   auto kern = q8_attn_rows_kernel<T, HD, FMT>;
   const cudaError_t e = configure_kernel((const void*)kern, RowCfg<HD>::kSmem, false);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(p.tiles * p.splits, p.n_kv, p.B), dim3(kRThreads), RowCfg<HD>::kSmem, stream, p);
+  const cudaError_t l =
+      launch_k(kern, dim3(p.tiles * p.splits, p.n_kv, p.B), dim3(kRThreads), RowCfg<HD>::kSmem, stream, p);
+  if (l != cudaSuccess || p.splits == 1) return l;
+  return launch_k(q8_attn_join_kernel<T, HD>, dim3(p.k * p.group, p.n_kv, p.B), dim3(kRThreads), 0, stream, p);
 }
 
 // Key shares of a row tile: as many CTAs as the SMs hold by shared memory (two
 // each for hd 128, four for 64: one token over 4 x 65536 tokens x 8 kv heads
 // of 64 72 against 89 us with two), each with a chunk for every warp, within
 // the scratch.
-static int rows_splits(const Q8AttnParams& p, int hd, int num_sms, size_t part_rows, size_t sync_len) {
+static int rows_splits(const Q8AttnParams& p, int hd, int num_sms, size_t part_rows) {
   const long long groups = (long long)p.B * p.n_kv * p.tiles;
-  const int most = (p.N + kRKeys * kRWarps - 1) / (kRKeys * kRWarps);
+  // (one or two chunks a warp unsplit: the join would cost more than they do,
+  // 7.1 against 5.9 us for 40 fp32 rows of N = 256)
+  const int most = p.N <= 2 * kRKeys * kRWarps ? 1 : (p.N + kRKeys * kRWarps - 1) / (kRKeys * kRWarps);
   long long s = (long long)(256 / hd) * num_sms / groups;
   s = s < most ? s : most;
   s = s < 64 ? s : 64;
-  if (groups > (long long)sync_len) s = 1;
   const long long fit = (long long)(part_rows / 16) / groups;
   s = s < fit ? s : fit;
   return s < 1 ? 1 : (int)s;
 }
 
+// Estimated time of the row kernel (us): its chunks one after the other in a
+// warp, slower as the SMs fill, and the join of the shares.
+static double rows_us(const Q8AttnParams& p, int hd, int num_sms) {
+  const double ctas = (double)p.B * p.n_kv * p.tiles * p.splits, places = (double)num_sms * (256 / hd);
+  const double chunks = (double)(((p.N + kRKeys - 1) / kRKeys + kRWarps * p.splits - 1) / (kRWarps * p.splits));
+  const double waves = ceil(ctas / places), load = ctas < places ? ctas / places : 1.0;
+  return hd == 128 ? 6.5 + (p.splits > 1 ? 1.8 : 0.0) + waves * chunks * (0.4 + 2.1 * load)
+                   : 4.1 + (p.splits > 1 ? 2.9 : 0.0) + waves * chunks * (0.4 + 1.9 * load);
+}
+
 cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, float* part, size_t part_floats,
-                                size_t sync_len, int num_sms, cudaStream_t stream) {
-  // More than one row tile: each key would be converted again for every 16
-  // query rows, which the tensor-core kernel does once for 128 or 256.  At
-  // N = 512, 32 heads of 128: 16 rows 15.7 (this kernel) against 15.5 us, 32
-  // rows 17.5 / 13.4, 128 rows 25.0 / 13.9 us; one row 8.5 / 13.2 us.
-  if (dtype == 1 && hd >= 64 && p.k * p.group > 16) return launch_q8_attention_tc(fmt, hd, p, num_sms, stream);
+                                int num_sms, cudaStream_t stream) {
   p.tiles = (p.k * p.group + 15) / 16;
   const size_t part_rows = part_floats / (hd + 2) / 16 * 16;
-  p.splits = rows_splits(p, hd, num_sms, part_rows, sync_len);
+  p.splits = rows_splits(p, hd, num_sms, part_rows);
+  // This kernel converts each key again for every 16 query rows; the
+  // tensor-core kernel does it once for 128 or 256, but has one CTA per SM, at
+  // most 8 key shares and a long step.  The estimates decide; their constants
+  // are a least-squares fit to both kernels' times at 181 sizes (1 to 256
+  // queries, N 128 to 8192, 2 to 256 kv heads), where the slower kernel is
+  // taken ten times and costs 28 % at most.  Both sides, us, this kernel
+  // first: B = 8, N = 2048, 32 kv heads of 128: 1 row 36 / 96, 32 rows 73 /
+  // 97, 64 rows 125 / 98; B = 1, N = 512: 16 rows 9.0 / 10.7, 32 rows 12.7 /
+  // 11.6; N = 8192, 2 kv heads, 7 rows 11 / 25, 448 rows 36 / 29.
+  if (dtype == 1 && hd >= 64 && q8_attention_tc_us(p, hd, num_sms) < rows_us(p, hd, num_sms))
+    return launch_q8_attention_tc(fmt, hd, p, num_sms, stream);
   p.part_o = part;
   p.part_ml = part + part_rows * hd;
 #define SPA_Q8_CASE(T_, HD_)                                                            \

@@ -574,13 +574,35 @@ static int tc_splits(long long ctas, int n_kt, int num_sms) {
   return s;
 }
 
-cudaError_t launch_q8_attention_tc(int fmt, int hd, Q8AttnParams p, int num_sms, cudaStream_t stream) {
-  const int n_kt = (p.N + kTK - 1) / kTK;
+// Query tiles per CTA, CTAs without key shares, key shares.
+struct TcPlan {
+  bool two;
+  long long ctas;
+  int splits;
+};
+static TcPlan tc_plan(const Q8AttnParams& p, int num_sms) {
+  TcPlan t;
   const long long heads = (long long)p.B * p.n_kv;
   const int t1 = (p.k * p.group + kTT - 1) / kTT, t2 = (t1 + 1) / 2;
   // two query tiles in a CTA share the converted keys and values; one while the single tiles do not fill the SMs
-  const bool two = t1 >= 2 && heads * t1 > num_sms / 2;
-  const int s = tc_splits(heads * (two ? t2 : t1), n_kt, num_sms);
+  t.two = t1 >= 2 && heads * t1 > num_sms / 2;
+  t.ctas = heads * (t.two ? t2 : t1);
+  t.splits = tc_splits(t.ctas, (p.N + kTK - 1) / kTK, num_sms);
+  return t;
+}
+
+double q8_attention_tc_us(const Q8AttnParams& p, int hd, int num_sms) {
+  const TcPlan t = tc_plan(p, num_sms);
+  const double rounds = (double)((t.ctas * t.splits + num_sms - 1) / num_sms);
+  const double steps = rounds * (double)(((p.N + kTK - 1) / kTK + t.splits - 1) / t.splits);
+  return hd == 128 ? 5.7 + (t.two ? 1.7 : 1.3) * steps + (t.splits > 1 ? 2.2 : 0.0)
+                   : 4.1 + (t.two ? 1.2 : 1.1) * steps + (t.splits > 1 ? 3.9 : 0.0);
+}
+
+cudaError_t launch_q8_attention_tc(int fmt, int hd, Q8AttnParams p, int num_sms, cudaStream_t stream) {
+  const TcPlan t = tc_plan(p, num_sms);
+  const bool two = t.two;
+  const int s = t.splits;
 #define SPA_TC_Q8(HD_, F_) \
   return two ? launch_tc<HD_, F_, 2>(p, s, stream) : launch_tc<HD_, F_, 1>(p, s, stream)
   if (hd == 128) {

@@ -344,6 +344,70 @@ def test_attention_f32(fmt, shape):
     check_attention(F32, fmt, B, N, heads, kv, hd, k, block, lens, seed=N + k)
 
 
+# Sizes that the tensor-core kernel takes by the dispatch's estimates: one and two query tiles per CTA, 1 to 8 key
+# shares, shared heads (7 and 4 to a kv head), odd sizes, padded batches.
+MANY_ROWS = [
+    (3, 1100, 8, 8, 128, 300, 64, None),
+    (2, 700, 14, 2, 128, 200, 16, None),
+    (1, 1537, 16, 4, 64, 256, 32, None),
+    (5, 333, 32, 8, 64, 200, 32, [333, 0, 1, 200, 332]),
+    (4, 200, 16, 16, 128, 150, 128, [0, 200, 128, 129]),
+    (1, 2100, 4, 2, 128, 500, 64, None),
+    (1, 190, 32, 32, 64, 300, 16, None),
+    (2, 577, 4, 4, 128, 256, 64, [577, 65]),
+    (8, 65, 16, 16, 128, 257, 32, [65, 64, 63, 1, 0, 33, 16, 17]),
+    (1, 1, 32, 32, 128, 300, 16, None),
+]
+
+
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("shape", MANY_ROWS)
+def test_attention_of_many_rows(fmt, shape):
+    B, N, heads, kv, hd, k, block, lens = shape
+    check_attention(BF16, fmt, B, N, heads, kv, hd, k, block, lens, seed=N * 3 + k)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_of_many_rows_keeps_to_its_rows_and_lengths(hd):
+    """The tensor-core kernel: NaN scales and codes past the lengths, and a NaN query, reach no other row; every
+    code comes through; the same bits again."""
+    rng = np.random.default_rng(13)
+    B, N, heads, k = 3, 300, 32, 150
+    ws = make_ws(BF16, heads, hd, B, N)
+    cache = spa.Q8Cache(B, N, heads, hd, block=32, fmt=E4M3)
+    fill_cache(rng, cache)
+    lens = [170, 64, 0]
+    q = torch.from_numpy(rng.standard_normal((B, k, heads, hd)).astype(np.float32)).to(torch.bfloat16).cuda()
+    ld = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    clean = run_attention(ws, cache, q, ld)
+    assert torch.equal(clean, run_attention(ws, cache, q, ld))
+    for b, n in enumerate(lens):
+        cache.k.view(torch.uint8)[b, n:] = 0x7F
+        cache.v.view(torch.uint8)[b, n:] = 0xFF
+        cache.k_scale[b, (n + 31) // 32:] = float("nan")
+        cache.v_scale[b, (n + 31) // 32:] = float("inf")
+    assert torch.equal(clean, run_attention(ws, cache, q, ld))
+    assert torch.count_nonzero(clean[2]) == 0
+    bad = q.clone()
+    bad[1, 77, 5, 9] = float("nan")
+    got = run_attention(ws, cache, bad, ld)
+    assert torch.isnan(got[1, 77, 5]).all()
+    keep = torch.ones((B, k, heads), dtype=torch.bool, device="cuda")
+    keep[1, 77, 5] = False
+    assert torch.equal(got[keep], clean[keep])
+    ws.check()
+    one = spa.Q8Cache(1, 1, heads, hd, block=16, fmt=E4M3)
+    codes = torch.arange(heads * hd, dtype=torch.int32).remainder(256).to(torch.uint8)
+    codes[(codes == 127) | (codes == 255)] = 0
+    one.v.view(torch.uint8).copy_(codes.view(1, 1, -1).cuda())
+    one.k.view(torch.uint8).copy_(codes.flip(0).view(1, 1, -1).cuda())
+    one.k_scale.fill_(2.0 ** -4)
+    one.v_scale.fill_(2.0 ** 3)
+    out = run_attention(ws, one, torch.randn((1, 300, heads, hd), device="cuda").to(torch.bfloat16))
+    V, _ = device_values(one, "v")
+    assert np.array_equal(np64(out), np.broadcast_to(V, out.shape))
+
+
 @pytest.mark.parametrize("hd,k", [(128, 1), (128, 200), (64, 140)])
 def test_attention_ignores_what_lies_past_the_length(hd, k):
     """NaN scales and codes behind a sequence's rows (and in the next sequences') do not reach its result."""
