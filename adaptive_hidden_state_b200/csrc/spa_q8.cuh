@@ -82,6 +82,21 @@ template <int FMT> __device__ __forceinline__ uint32_t q8_pair_f16(uint32_t x, u
   }
 }
 
+// Four codes of a word -> two f16 pairs.
+template <int FMT> __device__ __forceinline__ void q8_word_to_f16(uint32_t w, uint32_t& p01, uint32_t& p23) {
+  if constexpr (FMT == kQ8Int8) {
+    const uint32_t x = w ^ 0x80808080u, k = 0x64646464u, c = 0x64806480u;
+    const uint32_t a = __byte_perm(x, k, 0x4140), b = __byte_perm(x, k, 0x4342);
+    const __half2 h = *reinterpret_cast<const __half2*>(&c);
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), h), t = __hsub2(*reinterpret_cast<const __half2*>(&b), h);
+    p01 = *reinterpret_cast<const uint32_t*>(&r);
+    p23 = *reinterpret_cast<const uint32_t*>(&t);
+  } else {
+    p01 = q8_pair_f16<FMT>(w, w, 0, 1);
+    p23 = q8_pair_f16<FMT>(w, w, 2, 3);
+  }
+}
+
 // Asynchronous copies to shared memory; bytes 0: zeros, src is not read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");

@@ -137,13 +137,23 @@ __global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnPar
       const size_t off = (size_t)(key0 + pr) * width + pc * 16;
       const uint8_t *ks = kbase + off, *vs = vbase + off;
       const size_t step = (size_t)RPI * width;
+      const uint32_t d0 = smem_u32(dst);
+      if (key0 + kRKeys <= len) {
 #pragma unroll
-      for (int it = 0; it < STEPS; ++it) {
-        const uint32_t d = smem_u32(dst) + row_piece<HD>(pr + it * RPI, pc);
-        // rows past the end arrive as zeros and are not read
-        const bool ok = key0 + pr + it * RPI < len;
-        cp_async16(d, ok ? ks + it * step : kbase, ok ? 16 : 0);
-        cp_async16(d + kRKeys * HD, ok ? vs + it * step : vbase, ok ? 16 : 0);
+        for (int it = 0; it < STEPS; ++it) {
+          const uint32_t d = d0 + row_piece<HD>(pr + it * RPI, pc);
+          cp_async16(d, ks + it * step, 16);
+          cp_async16(d + kRKeys * HD, vs + it * step, 16);
+        }
+      } else {
+#pragma unroll
+        for (int it = 0; it < STEPS; ++it) {
+          const uint32_t d = d0 + row_piece<HD>(pr + it * RPI, pc);
+          // rows past the end arrive as zeros and are not read
+          const bool ok = key0 + pr + it * RPI < len;
+          cp_async16(d, ok ? ks + it * step : kbase, ok ? 16 : 0);
+          cp_async16(d + kRKeys * HD, ok ? vs + it * step : vbase, ok ? 16 : 0);
+        }
       }
       if (lane < 4) {  // key scales of keys 0-15 and 16-31, value scales
         const int key = min(key0 + 16 * (lane & 1), len - 1);
@@ -232,7 +242,8 @@ __global__ void __launch_bounds__(kRThreads) q8_attn_rows_kernel(const Q8AttnPar
       }
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
-        const uint32_t b0 = q8_pair_f16<FMT>(kw[i], kw[i], 0, 1), b1 = q8_pair_f16<FMT>(kw[i], kw[i], 2, 3);
+        uint32_t b0, b1;
+        q8_word_to_f16<FMT>(kw[i], b0, b1);
 #pragma unroll
         for (int n = 0; n < NT; ++n) mma_f16(s[t], q[n][i], b0, b1);
       }
