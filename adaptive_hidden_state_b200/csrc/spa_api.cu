@@ -1059,8 +1059,10 @@ static int run_q8_attention(spa_workspace* ws, const void* Q, const spa_q8_cache
   p.scale_log2 = 1.4426950408889634f / sqrtf((float)D.head_dim);
   const double q = 2.0 * c->B * k * D.d * (bf ? 2 : 4), kv = 2.0 * c->B * c->N * c->n_kv_heads * c->head_dim;
   ProfScope ps(&ws->prof, SPA_PROF_ATTN, q + kv, 4.0 * c->B * k * D.d * c->N, s);
+  int kernels = 1;
   const cudaError_t e = launch_q8_attention(bf, c->format, D.head_dim, p, ws->part_o, (size_t)ws->part_rows * D.d,
-                                            ws->num_sms, s);
+                                            ws->num_sms, &kernels, s);
+  g_launches += kernels - 1;
   if (e != cudaSuccess) return fail(SPA_ERR_CUDA, "8-bit cache attention launch: %s", cudaGetErrorString(e));
   return SPA_OK;
 }

@@ -307,9 +307,9 @@ struct Q8AttnParams {
 cudaError_t launch_q8_write(int dtype, int fmt, int block, Q8WriteParams p, int num_sms,
                             cudaStream_t stream);
 cudaError_t launch_q8_read(int dtype, int fmt, int block, Q8ReadParams p, cudaStream_t stream);
-// part: scratch for the key shares.
+// part: scratch for the key shares; kernels: how many it launched.
 cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, float* part, size_t part_floats,
-                                int num_sms, cudaStream_t stream);
+                                int num_sms, int* kernels, cudaStream_t stream);
 // The tensor-core kernel for many query rows (bf16, hd 64 or 128).
 cudaError_t launch_q8_attention_tc(int fmt, int hd, Q8AttnParams p, int num_sms, cudaStream_t stream);
 double q8_attention_tc_us(const Q8AttnParams& p, int hd, int num_sms);  // its estimated time

@@ -10,9 +10,9 @@
 //
 // The `top` largest: the running maxima of 64 groups of threads give a bound
 // that at least `top` logits reach, raised whenever the number of tiles read
-// has doubled; a thread compares the maximum of its 16 elements with it, and
-// the few elements that reach it (about 1.2 top in each doubling) go to their
-// warp's buffer in shared memory.  A buffer that fills keeps its best `top`.
+// is a power of four; a thread compares the maximum of its 16 elements with
+// it, and the few elements that reach it go to their warp's buffer in shared
+// memory.  A buffer that fills keeps its best `top`.
 // The order (larger value, then lower id) is total, and an entry's place is
 // the number of better ones, so the result depends on no timing.
 //
@@ -235,6 +235,11 @@ __device__ __forceinline__ void lp_unpack(const uint4 (&w)[U], float* v, int i, 
   }
 }
 
+// The bound is raised before tiles 0, 4, 16, 64, ... (at every doubling: 75.0 against 73.2 us for 768 x 126464).
+__device__ __forceinline__ bool raise_at(int tiles) {
+  return (tiles & (tiles - 1)) == 0 && (tiles == 0 || (tiles > 1 && (tiles & 0x55555555) != 0));
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads, 4) logp_kernel(const LogpParams p, int C) {
   constexpr int VN = LpVec<T>::N, U = 16 / VN;  // 16 elements a thread a tile
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logp_kernel(const LogpParams p,
   uint4 cur[U], nxt[U];
   constexpr int kStep = kLpThreads * U;
   lp_fetch<U>(nxt, xv, v0 + tid, v1);
-  int tiles = 0;  // read so far; the bound is raised whenever their number doubles
+  int tiles = 0;  // read so far
   // (one copy of the tile's code: straight-line code that runs once or twice waits for its instructions)
 #pragma unroll 1
   for (int b0 = v0; b0 < v1 || tiles == 0; b0 += kStep, ++tiles) {
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logp_kernel(const LogpParams p,
     lp_fetch<U>(nxt, xv, b0 + kStep + tid, v1);
     lp_unpack<T, U>(cur, v, b0 + tid, v1);
     lp_tile<U * VN, VN>(v, head + (b0 + tid) * VN, st, list, &s_cut, s_grp, top,
-                        top > 0 && (tiles & (tiles - 1)) == 0, warp, lane);
+                        top > 0 && raise_at(tiles), warp, lane);
   }
   if (warp == 0 && ((rank == 0 && head) || (rank == C - 1 && tail0 < p.V))) {
     // at most 7 elements on each side: lanes 0-15 before the vectors, 16-31 after them

@@ -487,7 +487,8 @@ static double rows_us(const Q8AttnParams& p, int hd, int num_sms) {
 }
 
 cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, float* part, size_t part_floats,
-                                int num_sms, cudaStream_t stream) {
+                                int num_sms, int* kernels, cudaStream_t stream) {
+  *kernels = 1;
   p.tiles = (p.k * p.group + 15) / 16;
   const size_t part_rows = part_floats / (hd + 2) / 16 * 16;
   p.splits = rows_splits(p, hd, num_sms, part_rows);
@@ -504,6 +505,7 @@ cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, floa
     return launch_q8_attention_tc(fmt, hd, p, num_sms, stream);
   p.part_o = part;
   p.part_ml = part + part_rows * hd;
+  *kernels = p.splits > 1 ? 2 : 1;
 #define SPA_Q8_CASE(T_, HD_)                                                            \
   if (hd == HD_)                                                                        \
     return fmt == kQ8Int8 ? launch_rows<T_, HD_, kQ8Int8>(p, stream) : launch_rows<T_, HD_, kQ8E4m3>(p, stream);
