@@ -301,6 +301,7 @@ struct Q8AttnParams {
   float *part_o, *part_ml;      // key shares: unnormalised rows, (m, l) pairs
   int* err;
   int B, k, N, n_heads, n_kv, group, block_log2, tiles, splits;
+  int item0;                    // tensor-core kernel: the launch's first (sequence, kv head, query tiles)
   float scale_log2;             // log2(e) / sqrt(hd)
 };
 // dtype 0 fp32, 1 bf16; fmt 0 int8, 1 e4m3; hd 32, 64 or 128; block 16, 32, 64 or 128.
@@ -311,7 +312,8 @@ cudaError_t launch_q8_read(int dtype, int fmt, int block, Q8ReadParams p, cudaSt
 cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, float* part, size_t part_floats,
                                 int num_sms, int* kernels, cudaStream_t stream);
 // The tensor-core kernel for many query rows (bf16, hd 64 or 128).
-cudaError_t launch_q8_attention_tc(int fmt, int hd, Q8AttnParams p, int num_sms, cudaStream_t stream);
+cudaError_t launch_q8_attention_tc(int fmt, int hd, Q8AttnParams p, int num_sms, int* kernels,
+                                   cudaStream_t stream);
 double q8_attention_tc_us(const Q8AttnParams& p, int hd, int num_sms);  // its estimated time
 // Per row of logits [rows, V] (row stride ld elements): log probability of
 // tok, entropy, and the `top` largest (ties to the lowest id).

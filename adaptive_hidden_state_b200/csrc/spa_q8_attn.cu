@@ -502,7 +502,7 @@ cudaError_t launch_q8_attention(int dtype, int fmt, int hd, Q8AttnParams p, floa
   // 97, 64 rows 125 / 98; B = 1, N = 512: 16 rows 9.0 / 10.7, 32 rows 12.7 /
   // 11.6; N = 8192, 2 kv heads, 7 rows 11 / 25, 448 rows 36 / 29.
   if (dtype == 1 && hd >= 64 && q8_attention_tc_us(p, hd, num_sms) < rows_us(p, hd, num_sms))
-    return launch_q8_attention_tc(fmt, hd, p, num_sms, stream);
+    return launch_q8_attention_tc(fmt, hd, p, num_sms, kernels, stream);
   p.part_o = part;
   p.part_ml = part + part_rows * hd;
   *kernels = p.splits > 1 ? 2 : 1;

@@ -39,6 +39,7 @@ namespace spa {
 constexpr int kTT = 128;                 // query rows of a tile
 constexpr int kTK = 64;                  // keys of a tile
 constexpr float kTRescale = 8.0f;
+constexpr int kTTailSteps = 6;           // fewest steps saved for which a launch gets a tail
 
 template <int HD, int NQ> struct TcCfg {
   static constexpr int kQBytes = kTT * HD * 2;        // one query tile
@@ -164,8 +165,11 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kConvWarp = NQ * 4, kMmaWarp = NQ * 4 + 4;
-  const int S = p.splits, sp = blockIdx.x % S, h = blockIdx.y, b = blockIdx.z;
-  const int row0 = (blockIdx.x / S) * NQ * kTT;  // first query row of this CTA
+  const int S = p.splits, sp = blockIdx.x & (S - 1);  // 1, 2, 4 or 8 key shares
+  // this CTA's (sequence, kv head, query tiles), the query tiles fastest
+  const unsigned item = (unsigned)p.item0 + (blockIdx.x >> (31 - __clz(S))), bh = item / (unsigned)p.tiles;
+  const int b = (int)(bh / (unsigned)p.n_kv), h = (int)(bh - (unsigned)b * p.n_kv);
+  const int row0 = (int)(item - bh * p.tiles) * NQ * kTT;  // first query row of this CTA
   const int R = p.k * p.group;
   int* err = p.err;
 
@@ -541,16 +545,18 @@ __global__ void __launch_bounds__(TcCfg<HD, NQ>::kThreads, 1) q8_attn_tc_kernel(
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
+// Items [item0, item0 + items), each with `splits` key shares.
 template <int HD, int FMT, int NQ>
-static cudaError_t launch_tc(Q8AttnParams& p, int splits_most, cudaStream_t stream) {
+static cudaError_t launch_tc(Q8AttnParams& p, int item0, int items, int splits, cudaStream_t stream) {
   using Cfg = TcCfg<HD, NQ>;
   auto kern = q8_attn_tc_kernel<HD, FMT, NQ>;
   cudaError_t e = configure_kernel((const void*)kern, Cfg::kSmem, false);
   if (e != cudaSuccess) return e;
-  p.splits = splits_most;
-  const int tiles = (p.k * p.group + NQ * kTT - 1) / (NQ * kTT);
+  p.splits = splits;
+  p.item0 = item0;
+  p.tiles = (p.k * p.group + NQ * kTT - 1) / (NQ * kTT);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * p.splits), p.n_kv, p.B);
+  cfg.gridDim = dim3((unsigned)items * (unsigned)splits);
   cfg.blockDim = dim3(Cfg::kThreads);
   cfg.dynamicSmemBytes = Cfg::kSmem;
   cfg.stream = stream;
@@ -574,47 +580,67 @@ static int tc_splits(long long ctas, int n_kt, int num_sms) {
   return s;
 }
 
-// Query tiles per CTA, CTAs without key shares, key shares.
+// Query tiles per CTA, CTAs without key shares, key shares.  Of more CTAs than
+// SMs the last `tail`, a round that would leave half of the SMs idle or more,
+// go into a launch of their own with `tail_splits` key shares, where that
+// saves at least kTTailSteps steps of a key tile (with a tail / without, us,
+// 32 heads of 128: B = 8, k = 512, N = 2048, 68 of 512 CTAs in two shares
+// 185 / 196; B = 5, k = 200, 12 of 160 CTAs in eight, N = 2048 70 / 99, N = 512,
+// 6 steps saved, 29.6 / 31.5; 4 steps saved, k = 512, B = 8, N = 512 71.7 / 70.3).
 struct TcPlan {
   bool two;
-  long long ctas;
-  int splits;
+  long long ctas, tail;
+  int splits, tail_splits;
+  double steps;  // of a key tile, one after the other
 };
 static TcPlan tc_plan(const Q8AttnParams& p, int num_sms) {
   TcPlan t;
   const long long heads = (long long)p.B * p.n_kv;
-  const int t1 = (p.k * p.group + kTT - 1) / kTT, t2 = (t1 + 1) / 2;
+  const int t1 = (p.k * p.group + kTT - 1) / kTT, t2 = (t1 + 1) / 2, n_kt = (p.N + kTK - 1) / kTK;
   // two query tiles in a CTA share the converted keys and values; one while the single tiles do not fill the SMs
   t.two = t1 >= 2 && heads * t1 > num_sms / 2;
   t.ctas = heads * (t.two ? t2 : t1);
-  t.splits = tc_splits(t.ctas, (p.N + kTK - 1) / kTK, num_sms);
+  t.splits = tc_splits(t.ctas, n_kt, num_sms);
+  const double rounds = (double)((t.ctas * t.splits + num_sms - 1) / num_sms);
+  t.steps = rounds * (double)((n_kt + t.splits - 1) / t.splits);
+  t.tail = t.ctas > num_sms ? t.ctas % num_sms : 0;
+  t.tail_splits = t.tail ? tc_splits(t.tail, n_kt, num_sms) : 1;
+  const int saved = n_kt - (n_kt + t.tail_splits - 1) / t.tail_splits;
+  if (saved >= kTTailSteps)
+    t.steps -= saved - 3;  // its launch and join cost about three
+  else
+    t.tail = 0;
   return t;
 }
 
 double q8_attention_tc_us(const Q8AttnParams& p, int hd, int num_sms) {
   const TcPlan t = tc_plan(p, num_sms);
-  const double rounds = (double)((t.ctas * t.splits + num_sms - 1) / num_sms);
-  const double steps = rounds * (double)(((p.N + kTK - 1) / kTK + t.splits - 1) / t.splits);
-  return hd == 128 ? 5.7 + (t.two ? 1.7 : 1.3) * steps + (t.splits > 1 ? 2.2 : 0.0)
-                   : 4.1 + (t.two ? 1.2 : 1.1) * steps + (t.splits > 1 ? 3.9 : 0.0);
+  return hd == 128 ? 5.7 + (t.two ? 1.7 : 1.3) * t.steps + (t.splits > 1 ? 2.2 : 0.0)
+                   : 4.1 + (t.two ? 1.2 : 1.1) * t.steps + (t.splits > 1 ? 3.9 : 0.0);
 }
 
-cudaError_t launch_q8_attention_tc(int fmt, int hd, Q8AttnParams p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_q8_attention_tc(int fmt, int hd, Q8AttnParams p, int num_sms, int* kernels, cudaStream_t stream) {
   const TcPlan t = tc_plan(p, num_sms);
-  const bool two = t.two;
-  const int s = t.splits;
-#define SPA_TC_Q8(HD_, F_) \
-  return two ? launch_tc<HD_, F_, 2>(p, s, stream) : launch_tc<HD_, F_, 1>(p, s, stream)
-  if (hd == 128) {
-    if (fmt == kQ8Int8) SPA_TC_Q8(128, kQ8Int8);
-    SPA_TC_Q8(128, kQ8E4m3);
-  }
-  if (hd == 64) {
-    if (fmt == kQ8Int8) SPA_TC_Q8(64, kQ8Int8);
-    SPA_TC_Q8(64, kQ8E4m3);
-  }
+  if (t.ctas * t.splits > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  *kernels = t.tail ? 2 : 1;
+  cudaError_t e = cudaErrorInvalidValue;
+#define SPA_TC_Q8(I0_, N_, S_)                                                                               \
+  if (hd == 128)                                                                                             \
+    e = fmt == kQ8Int8 ? (t.two ? launch_tc<128, kQ8Int8, 2>(p, I0_, N_, S_, stream)                         \
+                                : launch_tc<128, kQ8Int8, 1>(p, I0_, N_, S_, stream))                        \
+                       : (t.two ? launch_tc<128, kQ8E4m3, 2>(p, I0_, N_, S_, stream)                         \
+                                : launch_tc<128, kQ8E4m3, 1>(p, I0_, N_, S_, stream));                       \
+  else if (hd == 64)                                                                                         \
+    e = fmt == kQ8Int8 ? (t.two ? launch_tc<64, kQ8Int8, 2>(p, I0_, N_, S_, stream)                          \
+                                : launch_tc<64, kQ8Int8, 1>(p, I0_, N_, S_, stream))                         \
+                       : (t.two ? launch_tc<64, kQ8E4m3, 2>(p, I0_, N_, S_, stream)                          \
+                                : launch_tc<64, kQ8E4m3, 1>(p, I0_, N_, S_, stream));
+  const int most = (int)(t.ctas - t.tail);
+  SPA_TC_Q8(0, most, t.splits)
+  if (e != cudaSuccess || !t.tail) return e;
+  SPA_TC_Q8(most, (int)t.tail, t.tail_splits)
 #undef SPA_TC_Q8
-  return cudaErrorInvalidValue;
+  return e;
 }
 
 }  // namespace spa

@@ -202,6 +202,30 @@ def test_equal_and_outside_indices():
             assert np.array_equal(got[b, i], want)
 
 
+def test_equal_and_outside_indices_of_few_rows():
+    """Fewer rows than blocks: the first row of a block writes it."""
+    rng = np.random.default_rng(14)
+    B, N, kv, hd = 2, 200, 2, 64
+    ws = make_ws(BF16, heads_for(BF16, kv, hd), hd, B, N)
+    cache = spa.Q8Cache(B, N, kv, hd, block=16, fmt=INT8)
+    rk, rv = (RefCache(B, N, kv, hd, 16, INT8) for _ in range(2))
+    base = [rows_of(rng, (B, N, kv * hd), BF16) for _ in range(2)]
+    spa.spa_q8_write(ws, cache, base[0][0], base[1][0])
+    every = np.tile(np.arange(N), (B, 1))
+    rk.write(base[0][1], every)
+    rv.write(base[1][1], every)
+    idx = np.array([[199, 3, 199, 5, 3], [200, 0, -1, 0, 2 ** 31 - 1]], dtype=np.int32)
+    for _ in range(2):
+        kr, k64 = rows_of(rng, (B, 5, kv * hd), BF16)
+        vr, v64 = rows_of(rng, (B, 5, kv * hd), BF16)
+        spa.spa_q8_write(ws, cache, kr, vr, idx=torch.from_numpy(idx).cuda())
+        assert ws.status() == -7
+        rk.write(k64, idx)
+        rv.write(v64, idx)
+        check_cache(cache, rk, rv, "equal indices, few rows")
+    assert ws.status() == 0
+
+
 def test_values_a_cache_cannot_hold_are_reported():
     B, N, kv, hd = 1, 40, 1, 64
     ws = make_ws(F32, 1, hd, B, N)
@@ -358,6 +382,22 @@ MANY_ROWS = [
     (8, 65, 16, 16, 128, 257, 32, [65, 64, 63, 1, 0, 33, 16, 17]),
     (1, 1, 32, 32, 128, 300, 16, None),
 ]
+
+
+# More CTAs than SMs, the last ones in a launch of their own with key shares: eight, four and two of them.
+MANY_ROWS_TAIL = [
+    (5, 1030, 32, 32, 128, 150, 64, None),
+    (7, 1025, 24, 24, 64, 129, 32, [1025, 1024, 0, 1, 63, 64, 700]),
+    (3, 1090, 64, 32, 128, 130, 16, [1090, 5, 1089]),
+    (3, 777, 64, 64, 64, 140, 128, None),
+]
+
+
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("shape", MANY_ROWS_TAIL)
+def test_attention_of_many_rows_with_a_tail(fmt, shape):
+    B, N, heads, kv, hd, k, block, lens = shape
+    check_attention(BF16, fmt, B, N, heads, kv, hd, k, block, lens, seed=N * 5 + k)
 
 
 @pytest.mark.parametrize("fmt", [INT8, E4M3])
