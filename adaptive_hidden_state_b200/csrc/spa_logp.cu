@@ -172,8 +172,11 @@ __device__ __forceinline__ void lp_tile(const float (&x)[NE], int id0, LpStat& s
   if (NE % 2 == 0) tm = fmaxf(tm, x[NE - 1]);
   if (bound) lp_bound(fmaxf(tm, st.m), s_grp, s_cut, top, warp, lane);
   if (tm > st.m) {
-    const LpStat none = {tm, 0.f, 0.f};
-    st = lp_merge(st, none);
+    // against the new maximum; as in lp_merge
+    const float d = fmaxf((st.m - tm) * kLog2e, -1e4f), f = ex2(d);
+    st.t = f * fmaf(st.s, d, st.t);
+    st.s *= f;
+    st.m = tm;
   }
   const float ref = st.m == -INFINITY ? 0.f : st.m;
   // 2^-150 is 0 here; the bound keeps 0 * -inf out of t, and lets NaN pass
@@ -214,28 +217,27 @@ __device__ __forceinline__ void lp_tile(const float (&x)[NE], int id0, LpStat& s
   }
 }
 
-// Vectors i, i + one CTA's width, ... below v1.
-template <int U>
-__device__ __forceinline__ void lp_fetch(uint4 (&w)[U], const uint4* xv, int i, int v1) {
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (i + u * kLpThreads < v1) w[u] = __ldg(xv + i + u * kLpThreads);
-}
+// Vectors i = b0 + thread, i + one CTA's width, ... below v1; past it -inf.
+// (With the checks out of whole tiles and a re-scaling of its own in lp_tile,
+// 768 rows of 126464 bf16 63.8 -> 58.2 us, of 32003 fp32 26.8 -> 24.3; 126464
+// fp32, at HBM's rate, 73.4 / 74.2.)
 template <typename T, int U>
-__device__ __forceinline__ void lp_unpack(const uint4 (&w)[U], float* v, int i, int v1) {
-  constexpr int VN = LpVec<T>::N;
+__device__ __forceinline__ void lp_fetch(uint4 (&w)[U], const uint4* xv, int b0, int tid, int v1) {
+  const uint4* at = xv + b0 + tid;
+  if (b0 + U * kLpThreads <= v1) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (i + u * kLpThreads < v1) {
-      LpVec<T>::unpack(w[u], v + u * VN);
-    } else {
+    for (int u = 0; u < U; ++u) w[u] = __ldg(at + u * kLpThreads);
+  } else {
+    constexpr uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
 #pragma unroll
-      for (int e = 0; e < VN; ++e) v[u * VN + e] = -INFINITY;
+    for (int u = 0; u < U; ++u) {
+      w[u] = make_uint4(none, none, none, none);
+      if (b0 + tid + u * kLpThreads < v1) w[u] = __ldg(at + u * kLpThreads);
     }
   }
 }
 
-// The bound is raised before tiles 0, 4, 16, 64, ... (at every doubling: 75.0 against 73.2 us for 768 x 126464).
+// The bound is raised before tiles 0, 4, 16, 64, ... (at every doubling: 75.0 against 73.2 us, at the time, for 768 x 126464).
 __device__ __forceinline__ bool raise_at(int tiles) {
   return (tiles & (tiles - 1)) == 0 && (tiles == 0 || (tiles > 1 && (tiles & 0x55555555) != 0));
 }
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logp_kernel(const LogpParams p,
   // the next tile's loads are in flight while this one is worked on
   uint4 cur[U], nxt[U];
   constexpr int kStep = kLpThreads * U;
-  lp_fetch<U>(nxt, xv, v0 + tid, v1);
+  lp_fetch<T, U>(nxt, xv, v0, tid, v1);
   int tiles = 0;  // read so far
   // (one copy of the tile's code: straight-line code that runs once or twice waits for its instructions)
 #pragma unroll 1
@@ -284,8 +286,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) logp_kernel(const LogpParams p,
     float v[U * VN];
 #pragma unroll
     for (int u = 0; u < U; ++u) cur[u] = nxt[u];
-    lp_fetch<U>(nxt, xv, b0 + kStep + tid, v1);
-    lp_unpack<T, U>(cur, v, b0 + tid, v1);
+    if (b0 + kStep < v1) lp_fetch<T, U>(nxt, xv, b0 + kStep, tid, v1);
+#pragma unroll
+    for (int u = 0; u < U; ++u) LpVec<T>::unpack(cur[u], v + u * VN);
     lp_tile<U * VN, VN>(v, head + (b0 + tid) * VN, st, list, &s_cut, s_grp, top,
                         top > 0 && raise_at(tiles), warp, lane);
   }
@@ -403,9 +406,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) logp_kernel(const LogpParams p,
 
 cudaError_t launch_token_logprobs(int dtype, const LogpParams& p, int rows, int num_sms, cudaStream_t stream) {
   // CTAs per row: as many as the SMs hold at once (four each), each with at
-  // least a tile.  2 rows of 126464: 1 -> 8 CTAs 20.7 -> 9.7 us; 130 rows of
-  // 32003: 1 -> 4 14.9 -> 12.2 us, but 8 (two waves) 19.2 us; 768 rows of
-  // 126464: 1 -> 2 76.8 -> 82.7 us.
+  // least a tile.  At the time: 2 rows of 126464: 1 -> 8 CTAs 20.7 -> 9.7 us;
+  // 130 rows of 32003: 1 -> 4 14.9 -> 12.2 us, but 8 (two waves) 19.2 us; 768
+  // rows of 126464: 1 -> 2 76.8 -> 82.7 us, or 2 for the last 176 rows alone,
+  // which then wait for the others' end, 73.2 -> 76.0 us (32003 27.2 -> 32.2).
   int C = 1;
   while (C < 8 && (long long)rows * 2 * C <= 4LL * num_sms && p.V / (2 * C) >= 4096) C *= 2;
   cudaLaunchConfig_t cfg = {};
